@@ -1,0 +1,447 @@
+// grouped_sm100.cu - block-scaled FP4 products over groups of rows: the three
+// GEMMs of a linear layer whose weight is a stack of E experts and whose
+// tokens are sorted by expert, group e having any number m_e of rows (none,
+// too) that only the device knows (offsets, int32 [E + 1]).
+//
+// The activations are quantized in a padded layout: group e starts at row
+// p_e = sum_{i<e} 128 ceil(m_i / 128), the rows up to the next group are zero.
+// So a group starts at a whole 512-byte scale atom along the rows (Fprop,
+// Dgrad), and along the tokens (Wgrad) its blocks, rotations and 64-element
+// MMA steps hold no other group's tokens.
+//   rows:  D[off_e + i][n] = gA gB sum_k A[p_e + i][k] B_e[n][k], i < m_e.
+//          B_e is a part of B along its rows (Fprop: W as [E N x K]) or along
+//          the reduction axis (Dgrad: W^T as [K x E N]).
+//   wgrad: D[e] = gA gB sum over group e's tokens t of A[.][t] B[.][t]^T.
+//
+// The kernel is the dense CTA-pair kernel (256 x 256 tiles, tcgen05
+// cta_group::2, the same warp roles and rings) with another walk: every role
+// finds a tile's group by a binary search over prefix sums of the tile counts
+// in shared memory, which the CTA builds once from the offsets. A tile never
+// spans two groups. Rows of D past a group belong to the next one: 32-row
+// boxes that are full leave by TMA, the one a group's end cuts is written row
+// by row from the registers.
+#include "qfp4_device.cuh"
+#include "qfp4_internal.h"
+
+namespace qfp4 {
+namespace {
+
+// The groups as a CTA sees them: row[e] the first row of D, padded[e] the first
+// padded row, tiles[e] the number of 256-row tiles before group e.
+struct GroupTable {
+    int row[kMaxGroups + 1];
+    int padded[kMaxGroups + 1];
+    int tiles[kMaxGroups + 1];
+    __device__ __forceinline__ int size(int e) const { return row[e + 1] - row[e]; }
+};
+
+// Built by one warp. Offsets that fall anywhere or leave [0, T] would lead out
+// of the buffers: they raise the device error word and make every group empty.
+__device__ __forceinline__ void build_groups(GroupTable& g, const int* offsets, int E, int T, int lane) {
+    bool bad = false;
+    for (int e = lane; e <= E; e += 32) {
+        const int o = offsets[e];
+        bad = bad || o < 0 || o > T || (e < E && offsets[e + 1] < o);
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (bad && lane == 0 && blockIdx.x == 0) raise_device_error(DEV_ERR_OFFSETS);
+    int padded = 0, tiles = 0;  // of the groups before this step's 32
+    for (int e0 = 0; e0 <= E; e0 += 32) {
+        const int e = e0 + lane;
+        const int o = e <= E && !bad ? offsets[e] : 0;
+        const int m = e < E && !bad ? offsets[e + 1] - o : 0;
+        const int own_a = (m + 127) / 128, own_b = (m + 255) / 256;
+        int a = own_a, b = own_b;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int ua = __shfl_up_sync(0xffffffffu, a, s), ub = __shfl_up_sync(0xffffffffu, b, s);
+            if (lane >= s) {
+                a += ua;
+                b += ub;
+            }
+        }
+        if (e <= E) {
+            g.row[e] = o;
+            g.padded[e] = (padded + a - own_a) * 128;
+            g.tiles[e] = tiles + b - own_b;
+        }
+        padded += __shfl_sync(0xffffffffu, a, 31);
+        tiles += __shfl_sync(0xffffffffu, b, 31);
+    }
+}
+
+// The group of padded row r, or -1 past the last.
+__device__ __forceinline__ int group_of(const int* first, int E, int r) {
+    if (r >= first[E]) return -1;
+    int lo = 0, hi = E;  // first[lo] <= r < first[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= r) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// One tile of the walk.
+struct GroupTile {
+    int e;       // group
+    int m0, n0;  // first row (within the group, or of its D in wgrad) and column
+    int k0, k;   // first element of the reduction in A, its length
+};
+
+template <bool WGRAD>
+struct GroupWalk {
+    const GroupTable& g;
+    const GroupedParams& p;
+    int num_m, num_n, total;
+    __device__ __forceinline__ GroupWalk(const GroupTable& t, const GroupedParams& q) : g(t), p(q) {
+        num_n = (p.N + kGemmBN - 1) / kGemmBN;
+        num_m = WGRAD ? (p.M + 255) / 256 : 0;
+        total = WGRAD ? p.E * num_m * num_n : g.tiles[p.E] * num_n;
+    }
+    // Within a group the row tiles run fastest: concurrent CTAs share the
+    // group's B tiles in L2.
+    __device__ __forceinline__ GroupTile at(int t) const {
+        GroupTile r;
+        if constexpr (WGRAD) {
+            const int per = num_m * num_n, i = t % per;
+            r.e = t / per;
+            r.m0 = (i % num_m) * 256;
+            r.n0 = (i / num_m) * kGemmBN;
+            r.k0 = g.padded[r.e];
+            r.k = g.padded[r.e + 1] - r.k0;
+        } else {
+            r.e = group_of(g.tiles, p.E, t / num_n);
+            const int first = g.tiles[r.e], tm = g.tiles[r.e + 1] - first, i = t - first * num_n;
+            r.m0 = (i % tm) * 256;
+            r.n0 = (i / tm) * kGemmBN;
+            r.k0 = 0;
+            r.k = p.K;
+        }
+        return r;
+    }
+};
+
+// Rows cut by a group's end: this lane's 32 words (128 bytes) of its row to D
+// from column x, by 16-byte stores (N is a multiple of 8).
+__device__ __forceinline__ void store_row_words(const GroupedParams& p, const uint32_t* v, int64_t row, int x) {
+    const int esz = p.out_f32 ? 4 : 2, per = 16 / esz;
+    uint8_t* d = static_cast<uint8_t*>(p.D) + (row * p.ldd + x) * esz;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (x + j * per < p.N)
+            __stcs(chk(reinterpret_cast<uint4*>(d + 16 * j), p.D, ((int64_t)(p.T - 1) * p.ldd + p.N) * esz),
+                   make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+}
+
+// Epilogue of one tile for one warp: 32 rows x 128 columns from D row `row`, nv
+// of the rows stored; zero: the sum of an empty group.
+template <typename Release>
+__device__ __forceinline__ void group_epilogue(const GroupedParams& p, const CUtensorMap* tmD, uint32_t taddr,
+                                               int64_t row, int nv, int n0, float scale, bool zero, uint32_t obox,
+                                               int lane, Release release) {
+    const uint32_t rbase = obox + (uint32_t)lane * 128u;
+    // 32 words (128 bytes) of each lane's row, from column x: a whole box of 32
+    // rows through shared memory (128-byte swizzle) by TMA, which clips the
+    // columns past N
+    auto box = [&](const uint32_t* v, int x) {
+        if (nv < 32) {
+            if (lane < nv) store_row_words(p, v, row + lane, x);
+            return;
+        }
+        if (lane == 0) bulk_wait_group_read0();
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            sts128(rbase + ((uint32_t)(j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0 && x < p.N) {
+            if (p.accumulate)
+                tma_reduce_add_2d(tmD, obox, x, (int)row);
+            else
+                tma_store_2d(tmD, obox, x, (int)row);
+            bulk_commit_group();
+        }
+    };
+    if (!p.out_f32) {
+        uint32_t w[64];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t acc[64];
+            tmem_ld_32x32b_x32(taddr + 64 * h, acc);
+            tmem_ld_32x32b_x32(taddr + 64 * h + 32, acc + 32);
+            tc_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) w[32 * h + c] = zero ? 0u : pack_bf16(acc[2 * c], acc[2 * c + 1], scale);
+        }
+        tc_fence_before();
+        __syncwarp();
+        release();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) box(w + 32 * h, n0 + 64 * h);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t acc[64];
+            tmem_ld_32x32b_x32(taddr + 64 * h, acc);
+            tmem_ld_32x32b_x32(taddr + 64 * h + 32, acc + 32);
+            tc_wait_ld();
+            if (h == 1) {
+                tc_fence_before();
+                __syncwarp();
+                release();
+            }
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+                const float2 v = __fmul2_rn(make_float2(__uint_as_float(acc[c]), __uint_as_float(acc[c + 1])),
+                                            make_float2(scale, scale));
+                acc[c] = zero ? 0u : __float_as_uint(v.x);
+                acc[c + 1] = zero ? 0u : __float_as_uint(v.y);
+            }
+            box(acc, n0 + 64 * h);
+            box(acc + 32, n0 + 64 * h + 32);
+        }
+    }
+}
+
+constexpr int GP_SMEM = P_SMEM + (int)sizeof(GroupTable);
+static_assert(GP_SMEM <= 227 * 1024, "shared memory of one CTA");
+
+template <int FMT, bool WGRAD>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+    gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmSFA, const __grid_constant__ CUtensorMap tmSFB,
+                        const __grid_constant__ CUtensorMap tmD, const GroupedParams p) {
+    constexpr int SF_K = (FMT == kNvfp4) ? 64 : 128;
+    constexpr int ATOMS_PER_KT = BK / SF_K;  // 4 or 2
+    constexpr uint32_t AB_TX = 2u * (P_A + P_B);          // both CTAs, on the leader
+    constexpr uint32_t SF_TX = 3u * ATOMS_PER_KT * 512u;  // this CTA's scale boxes
+    extern __shared__ __align__(1024) uint8_t dyn_smem[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
+    uint8_t* sA = base;
+    uint8_t* sB = sA + P_STAGES * P_A;
+    uint8_t* sSFA = sB + P_STAGES * P_B;
+    uint8_t* sSFB = sSFA + P_STAGES * P_SFA;
+    uint8_t* sOut = sSFB + P_STAGES * P_SFB;  // kEpiWarps boxes, 1024-byte aligned
+    uint64_t* full = reinterpret_cast<uint64_t*>(sOut + kEpiWarps * P_OUT_BOX);
+    uint64_t* empty = full + P_STAGES;
+    uint64_t* sf_load = empty + P_STAGES;    // this CTA's scale atoms of stage s landed
+    uint64_t* sf_full = sf_load + P_STAGES;  // scale slot s written in both CTAs (leader's)
+    uint64_t* acc_full = sf_full + P_STAGES;
+    uint64_t* acc_empty = acc_full + 1;
+    uint64_t* drain = acc_empty + 1;  // every MMA the leader issued has completed (both CTAs)
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    GroupTable& groups = *reinterpret_cast<GroupTable*>(sOut + kEpiWarps * P_OUT_BOX + 512);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int cid = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmB);
+        prefetch_tmap(&tmSFA);
+        prefetch_tmap(&tmSFB);
+        prefetch_tmap(&tmD);
+        for (int s = 0; s < P_STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+            mbar_init(&sf_load[s], 1);
+            mbar_init(&sf_full[s], 2 * kScaleWarps);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 2 * kEpiWarps);
+        mbar_init(drain, 1);
+        fence_mbarrier_init();
+    }
+    if (warp == 0) tmem_alloc_pair(tmem_slot, TMEM_COLS);
+    pdl_wait();  // the offsets and the operands are written (and the previous readers of D done)
+    pdl_launch_dependents();
+    if (warp == 1) build_groups(groups, p.offsets, p.E, p.T, lane);
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();  // barriers of both CTAs initialised, tensor memory allocated, groups known
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const GroupWalk<WGRAD> walk(groups, p);
+
+    if (warp == 0) {
+        // ---------------- TMA producer (both CTAs) ----------------
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int t = cid; t < walk.total && ok; t += nclusters) {
+                const GroupTile w = walk.at(t);
+                const int arow = (WGRAD ? 0 : groups.padded[w.e]) + w.m0 + (int)rank * BM;
+                const int brow = (WGRAD ? 0 : w.e * p.b_rows) + w.n0;
+                const int bk0 = WGRAD ? w.k0 : w.e * p.b_k;
+                const int kt_n = (w.k + BK - 1) / BK;
+                for (int kt = 0; kt < kt_n; ++kt, ++it) {
+                    const int s = it % P_STAGES;
+                    if (it >= P_STAGES && !mbar_wait_cluster(&empty[s], ((it / P_STAGES) + 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&sf_load[s], SF_TX);
+                    tma_load_3d(sSFA + s * P_SFA, &tmSFA, &sf_load[s], 0, w.k0 / SF_K + kt * ATOMS_PER_KT, arow / 128);
+                    tma_load_3d(sSFB + s * P_SFB, &tmSFB, &sf_load[s], 0, bk0 / SF_K + kt * ATOMS_PER_KT, brow / 128);
+                    const uint32_t bar_leader = mapa_shared(smem_u32(&full[s]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], AB_TX);
+                    tma_load_2d_pair(sA + s * P_A, &tmA, bar_leader, w.k0 / 2 + kt * (BK / 2), arow);
+                    tma_load_2d_pair(sB + s * P_B, &tmB, bar_leader, bk0 / 2 + kt * (BK / 2), brow + (int)rank * 128);
+                }
+            }
+            drain_loads(rank == 0 ? full : nullptr, sf_load, P_STAGES, it);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (leader CTA only) ----------------
+        if (lane == 0 && rank == 0) {
+            const uint64_t a_desc0 = sw128_desc(smem_u32(sA)), b_desc0 = sw128_desc(smem_u32(sB));
+            int s = 0, lt = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int t = cid; t < walk.total && ok; t += nclusters, ++lt) {
+                const GroupTile w = walk.at(t);
+                if (lt > 0 && !mbar_wait_cluster(acc_empty, (lt - 1) & 1)) break;
+                tc_fence_after();
+                for (int k = 0; k < w.k; k += BK) {
+                    if (!mbar_wait_cluster(&sf_full[s], ph)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    mma_ktile<FMT, true, 2 * BM>(tmem + TMEM_D, a_desc0 + (uint64_t)(s * (P_A >> 4)),
+                                                 b_desc0 + (uint64_t)(s * (P_B >> 4)), tmem + sfa_col(s),
+                                                 tmem + sfb_col(s), min(BK, w.k - k) / 64, k == 0);
+                    tc_commit_pair(&empty[s]);  // frees stage s and scale slot s in both CTAs
+                    if (++s == P_STAGES) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+                tc_commit_pair(acc_full);  // both CTAs' accumulators are complete
+            }
+            tc_commit_pair(drain);
+            (void)mbar_wait(drain, 0);
+        }
+    } else if (warp < kFirstEpiWarp) {
+        // ---------------- scale writers (both CTAs) ----------------
+        const uint32_t tmem_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int t = cid; t < walk.total && ok; t += nclusters) {
+            const int k_len = walk.at(t).k;
+            for (int k = 0; k < k_len; k += BK) {
+                if (!mbar_wait_cluster(&sf_load[s], ph)) {
+                    ok = false;
+                    break;
+                }
+                write_scales<ATOMS_PER_KT>(tmem_lane, s, smem_u32(sSFA + s * P_SFA), smem_u32(sSFB + s * P_SFB), lane,
+                                           warp & 3);
+                if (rank == 0 && !mbar_wait_cluster(&full[s], ph)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sf_full[s]), 0));
+                if (++s == P_STAGES) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+    } else {
+        // ---------------- epilogue (both CTAs) ----------------
+        const int lq = warp & 3;
+        const int chalf = (warp - kFirstEpiWarp) >> 2;
+        const float scale = __fmul_rn(__ldg(p.ga), __ldg(p.gb));
+        const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
+        const uint32_t obox = smem_u32(sOut) + (uint32_t)(warp - kFirstEpiWarp) * P_OUT_BOX;
+        int lt = 0;
+        for (int t = cid; t < walk.total; t += nclusters, ++lt) {
+            const GroupTile w = walk.at(t);
+            if (!mbar_wait_cluster(acc_full, lt & 1)) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem + ((uint32_t)(lq * 32) << 16) + TMEM_D + chalf * 128;
+            const int m = w.m0 + (int)rank * BM + lq * 32;  // within the group
+            const int nv = min(32, (WGRAD ? p.M : groups.size(w.e)) - m);
+            const int64_t row = (WGRAD ? (int64_t)w.e * p.M : groups.row[w.e]) + m;
+            // an empty group's weight gradient is zero; added to D it changes nothing
+            group_epilogue(p, &tmD, taddr, row, w.k == 0 && p.accumulate ? 0 : nv, w.n0 + chalf * 128, scale,
+                           w.k == 0, obox, lane, [&] {
+                               if (lane == 0) mbar_arrive_cluster(acc_empty_leader);
+                           });
+        }
+        if (lane == 0) bulk_wait_group0();  // this warp's stores are complete
+    }
+
+    tc_fence_before();
+    cluster_sync();  // no CTA leaves while its peer may still signal it
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+}
+
+// xp = the groups' rows of x in the padded layout, zeros in every other row.
+// A warp copies whole rows, 16 bytes per lane and step.
+__global__ void __launch_bounds__(256) group_pad_kernel(const uint4* x, int64_t ld16, int64_t c16, const int* offsets,
+                                                        int E, int T, int Tp, uint4* xp) {
+    __shared__ GroupTable g;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0) build_groups(g, offsets, E, T, lane);
+    __syncthreads();
+    const int64_t extent = (int64_t)Tp * c16 * 16;
+    for (int r = blockIdx.x * 8 + warp; r < Tp; r += gridDim.x * 8) {
+        const int e = group_of(g.padded, E, r);
+        const int i = e < 0 ? 0 : r - g.padded[e];
+        const bool have = e >= 0 && i < g.size(e);
+        const uint4* src = x + (have ? (int64_t)(g.row[e] + i) * ld16 : 0);
+        uint4* dst = xp + (int64_t)r * c16;
+#pragma unroll 4
+        for (int64_t c = lane; c < c16; c += 32) {
+            const uint4 v = have ? src[c] : make_uint4(0, 0, 0, 0);
+            *chk(dst + c, xp, extent) = v;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_grouped(const GroupedParams& p, int fmt, bool wgrad, const CUtensorMap* tmapA,
+                                const CUtensorMap* tmapB, const CUtensorMap* tmapSFA, const CUtensorMap* tmapSFB,
+                                const CUtensorMap* tmapD, cudaStream_t s, int sms) {
+    // the tile count is known on the device only: an upper bound sizes the grid
+    const int64_t num_n = (p.N + kGemmBN - 1) / kGemmBN;
+    const int64_t num_m = wgrad ? (int64_t)p.E * ((p.M + 255) / 256) : std::min<int64_t>(p.T, p.T / 256 + p.E);
+    const int clusters = (int)std::max<int64_t>(1, std::min<int64_t>(sms / 2, num_m * num_n));
+    auto run = [&](auto* kern) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GP_SMEM);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(kern, dim3(2 * clusters), dim3(kGemmThreads), GP_SMEM, s, *tmapA, *tmapB, *tmapSFA, *tmapSFB,
+                          *tmapD, p);
+    };
+    cudaError_t e;
+    if (fmt == kNvfp4)
+        e = wgrad ? run(gemm_grouped_kernel<kNvfp4, true>) : run(gemm_grouped_kernel<kNvfp4, false>);
+    else
+        e = wgrad ? run(gemm_grouped_kernel<kMxfp4, true>) : run(gemm_grouped_kernel<kMxfp4, false>);
+    count_launch();
+    return e;
+}
+
+cudaError_t launch_group_pad(const void* x, int64_t ld, int64_t C, const int* offsets, int E, int T, int Tp, void* xp,
+                             int sms, cudaStream_t s) {
+    const int grid = (int)std::min<int64_t>((Tp + 7) / 8, (int64_t)sms * 8);
+    const cudaError_t e = launch_pdl(group_pad_kernel, dim3(grid), dim3(256), 0, s, static_cast<const uint4*>(x), ld / 8,
+                                     C / 8, offsets, E, T, Tp, static_cast<uint4*>(xp));
+    count_launch();
+    return e;
+}
+
+}  // namespace qfp4

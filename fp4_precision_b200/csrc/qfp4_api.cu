@@ -9,6 +9,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
@@ -802,6 +803,7 @@ const char* qfp4_strerror(int status) {
         case QFP4_ERR_TIMEOUT: return "device-side bounded wait expired";
         case QFP4_ERR_BOUNDS: return "bounds-checked build: a kernel store fell outside its buffer";
         case QFP4_ERR_TOO_LARGE: return "problem exceeds the fixed scratch of qfp4_linear_fwd_noalloc (32 MiB)";
+        case QFP4_ERR_OFFSETS: return "group offsets fall or leave their rows";
         default: return "unknown status";
     }
 }
@@ -984,6 +986,45 @@ int linear_fwd_impl(const void* X, const void* W, void* Y, int64_t M, int64_t N,
     const AmaxOut ao{next_had, &ns, y_amax, partials, pws};
     return gemm_impl(&t[0], &t[1], Y, N, QFP4_OUT_BF16, false, s, nullptr, &ao);
 }
+
+// dY (M x N, contiguous) quantized along N for Dgrad into out_row, and for
+// Wgrad along M into out_col where one read gives both: then *col_done is set,
+// else *am_col is what the column quantization takes. When both are NVFP4 with the same
+// Hadamard (size <= 16; the sign vectors differ per GEMM), one read of dY gives
+// both tensor amaxes. When both quantizations round to nearest with the same
+// format, one more read gives both quantized operands (memory-bound, so one
+// read instead of two is a quarter faster); stochastic and Quartet II rounding
+// are bound by instruction issue, and there the two separate passes are faster.
+// dy_amax: two floats; partials: the quantizers' workspace.
+int quantize_dy(const void* dY, int64_t M, int64_t N, const qfp4_recipe* recipe, const qfp4_seed* seed,
+                qfp4_tensor* out_row, qfp4_tensor* out_col, float* dy_amax, float* partials, bool* col_done,
+                const float** am_col, cudaStream_t s) {
+    const size_t pws = qfp4_quantize_workspace_bytes();
+    const qfp4_gemm_cfg& d = recipe->dgrad;
+    const qfp4_gemm_cfg& w = recipe->wgrad;
+    const qfp4_seed s0 = op_seed(seed, 1, 2), s2 = op_seed(seed, 2, 4);
+    const bool dual = d.fmt == w.fmt && d.rnd_a == QFP4_RTN && w.rnd_a == QFP4_RTN && dual_ok(M, d.had, w.had) &&
+                      col_bands_enabled();
+    const float* am_row = nullptr;
+    *am_col = nullptr;
+    *col_done = dual;
+    int rc;
+    if (d.fmt == QFP4_NVFP4 && w.fmt == QFP4_NVFP4 && d.had == w.had && had_n(d.had) <= 16) {
+        if ((rc = amax_rowcol_impl(dY, M, N, N, d.had, d.had, &s0, &s2, dy_amax, dy_amax + 1, partials, pws, s)))
+            return rc;
+        am_row = dy_amax;
+        *am_col = dy_amax + 1;
+    } else if (dual && d.fmt == QFP4_NVFP4) {
+        if ((rc = qfp4_amax(dY, M, N, N, d.had, QFP4_AXIS_ROW, &s0, dy_amax, partials, pws, s))) return rc;
+        if ((rc = qfp4_amax(dY, M, N, N, w.had, QFP4_AXIS_COL, &s2, dy_amax + 1, partials, pws, s))) return rc;
+        am_row = dy_amax;
+        *am_col = dy_amax + 1;
+    }
+    if (dual)
+        return quantize_dual_impl(dY, M, N, N, d.fmt, d.rnd_a, d.had, w.had, &s0, &s2, am_row, *am_col, out_row,
+                                  out_col, s);
+    return quantize_impl(dY, M, N, N, d.fmt, d.rnd_a, d.had, QFP4_AXIS_ROW, &s0, am_row, out_row, partials, pws, s);
+}
 }  // namespace
 }  // namespace qfp4
 
@@ -1024,49 +1065,485 @@ int qfp4_linear_bwd(const void* dY, const void* X, const void* W, void* dX, void
     const size_t pws = qfp4_quantize_workspace_bytes();
     const qfp4_gemm_cfg& d = recipe->dgrad;
     const qfp4_gemm_cfg& w = recipe->wgrad;
-    qfp4_seed s0 = op_seed(seed, 1, 2), s1 = op_seed(seed, 1, 3);
-    qfp4_seed s2 = op_seed(seed, 2, 4), s3 = op_seed(seed, 2, 5);
-    // dY is quantized along both axes (Dgrad: along N; Wgrad: along M). When
-    // both are NVFP4 with the same Hadamard (size <= 16; the sign vectors
-    // differ per GEMM), one read of dY gives both tensor amaxes. When both
-    // quantizations round to nearest with the same format, one more read gives
-    // both quantized operands (memory-bound, so one read instead of two is a
-    // quarter faster); stochastic and Quartet II rounding are bound by
-    // instruction issue, and there the two separate passes are faster.
-    const bool dual = d.fmt == w.fmt && d.rnd_a == QFP4_RTN && w.rnd_a == QFP4_RTN && dual_ok(M, d.had, w.had) &&
-                      col_bands_enabled();
-    const float* am_row = nullptr;
-    const float* am_col = nullptr;
-    if (d.fmt == QFP4_NVFP4 && w.fmt == QFP4_NVFP4 && d.had == w.had && had_n(d.had) <= 16) {
-        if ((rc = amax_rowcol_impl(dY, M, N, N, d.had, d.had, &s0, &s2, dy_amax, dy_amax + 1, partials, pws, s)))
-            return rc;
-        am_row = dy_amax;
-        am_col = dy_amax + 1;
-    } else if (dual && d.fmt == QFP4_NVFP4) {
-        if ((rc = qfp4_amax(dY, M, N, N, d.had, QFP4_AXIS_ROW, &s0, dy_amax, partials, pws, s))) return rc;
-        if ((rc = qfp4_amax(dY, M, N, N, w.had, QFP4_AXIS_COL, &s2, dy_amax + 1, partials, pws, s))) return rc;
-        am_row = dy_amax;
-        am_col = dy_amax + 1;
-    }
+    const qfp4_seed s1 = op_seed(seed, 1, 3), s2 = op_seed(seed, 2, 4), s3 = op_seed(seed, 2, 5);
+    bool dy_done;
+    const float* dy_am_col;
     // Dgrad dX[M,K] = dY[M,N] . W[N,K]: reduce over N.
-    if (dual) {
-        if ((rc = quantize_dual_impl(dY, M, N, N, d.fmt, d.rnd_a, d.had, w.had, &s0, &s2, am_row, am_col, &t[0],
-                                     &t[2], s)))
-            return rc;
-    } else if ((rc = quantize_impl(dY, M, N, N, d.fmt, d.rnd_a, d.had, QFP4_AXIS_ROW, &s0, am_row, &t[0], partials,
-                                   pws, s))) {
+    if ((rc = quantize_dy(dY, M, N, recipe, seed, &t[0], &t[2], dy_amax, partials, &dy_done, &dy_am_col, s)))
         return rc;
-    }
     if ((rc = quantize_impl(W, N, K, K, d.fmt, d.rnd_b, d.had, QFP4_AXIS_COL, &s1, nullptr, &t[1], partials, pws, s)))
         return rc;
     if ((rc = gemm_impl(&t[0], &t[1], dX, K, recipe->dx_dtype, false, s))) return rc;
     // Wgrad dW[N,K] = dY^T[N,M] . X[M,K]: reduce over M (tokens).
-    if (!dual &&
-        (rc = quantize_impl(dY, M, N, N, w.fmt, w.rnd_a, w.had, QFP4_AXIS_COL, &s2, am_col, &t[2], partials, pws, s)))
+    if (!dy_done && (rc = quantize_impl(dY, M, N, N, w.fmt, w.rnd_a, w.had, QFP4_AXIS_COL, &s2, dy_am_col, &t[2],
+                                        partials, pws, s)))
         return rc;
     if ((rc = quantize_impl(X, M, K, K, w.fmt, w.rnd_b, w.had, QFP4_AXIS_COL, &s3, nullptr, &t[3], partials, pws, s)))
         return rc;
     return gemm_impl(&t[2], &t[3], dW, K, recipe->dw_dtype, recipe->dw_accumulate != 0, s);
+}
+
+}  // extern "C"
+
+namespace qfp4 {
+namespace {
+// ---- RMSNorm ------------------------------------------------------------------
+// One bf16 R x C operand with row stride ld.
+int check_matrix(const void* x, int64_t R, int64_t C, int64_t ld) {
+    if (ld < C) return QFP4_ERR_INVALID_ARG;
+    if (R == 0) return QFP4_OK;
+    if (x == nullptr) return QFP4_ERR_INVALID_ARG;
+    return aligned16(x) && ld % 8 == 0 ? QFP4_OK : QFP4_ERR_MISALIGNED;
+}
+
+int check_norm(const void* w, int64_t R, int64_t C) {
+    if (R < 0 || R > 0x7fffffffLL || C <= 0 || C > QFP4_RMSNORM_MAX_COLS || C % 16 != 0) return QFP4_ERR_INVALID_ARG;
+    if (w == nullptr) return QFP4_ERR_INVALID_ARG;
+    return aligned16(w) ? QFP4_OK : QFP4_ERR_MISALIGNED;
+}
+
+// The arguments that both forward calls share; fills p.
+int norm_fwd_args(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* w, int64_t R, int64_t C,
+                  float eps, void* h, int64_t ldh, void* y, int64_t ldy, float* rstd, int32_t had,
+                  const qfp4_seed* seed, NormParams* p) {
+    int rc = check_norm(w, R, C);
+    if (rc) return rc;
+    if (!(eps >= 0.0f) || std::isinf(eps)) return QFP4_ERR_INVALID_ARG;
+    if (had < QFP4_HAD_NONE || had > QFP4_HAD_RAND32 || (had_n(had) != 0 && C % had_n(had) != 0))
+        return QFP4_ERR_INVALID_ARG;
+    if (had_random(had) && (seed == nullptr || seed->rot_stream >= (1u << 28))) return QFP4_ERR_INVALID_ARG;
+    if ((rc = check_matrix(x, R, C, ldx))) return rc;
+    if (res != nullptr && (rc = check_matrix(res, R, C, ldres))) return rc;
+    if ((res != nullptr || h != nullptr) && (rc = check_matrix(h, R, C, ldh))) return rc;
+    if (y != nullptr && (rc = check_matrix(y, R, C, ldy))) return rc;
+    if (R > 0 && rstd == nullptr) return QFP4_ERR_INVALID_ARG;
+    p->x = static_cast<const uint16_t*>(x);
+    p->res = static_cast<const uint16_t*>(res);
+    p->w = static_cast<const uint16_t*>(w);
+    p->ldx = ldx; p->ldres = ldres; p->R = R; p->C = C;
+    p->eps = (double)eps;
+    p->inv_c = 1.0 / (double)C;
+    p->h = static_cast<uint16_t*>(h);
+    p->y = static_cast<uint16_t*>(y);
+    p->ldh = ldh; p->ldy = ldy;
+    p->rstd = rstd;
+    p->signs = had_random(had) ? host_sign_bits(seed->rot, seed->rot_stream) : 0u;
+    return QFP4_OK;
+}
+
+int set_zero(float* v, int64_t n, cudaStream_t s) {
+    const cudaError_t e = cudaMemsetAsync(v, 0, (size_t)n * sizeof(float), s);
+    return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
+}
+
+// ---- groups of rows -------------------------------------------------------------
+// Rows of the padded layout: what T rows in E groups, at most min(E, T) of them
+// not empty, can need. A multiple of 128.
+int64_t group_rows(int64_t T, int32_t E) {
+    return T <= 0 ? 0 : (T + 127 * std::min<int64_t>(E, T)) / 128 * 128;
+}
+
+int check_groups(const int32_t* offsets, int32_t E, int64_t T) {
+    if (E < 1 || E > QFP4_MAX_GROUPS || T < 0 || T > 0x7fffffffLL) return QFP4_ERR_INVALID_ARG;
+    if (group_rows(T, E) > 0x7fffffffLL || offsets == nullptr) return QFP4_ERR_INVALID_ARG;
+    return reinterpret_cast<uintptr_t>(offsets) % 4 == 0 ? QFP4_OK : QFP4_ERR_MISALIGNED;
+}
+
+// The operand pair of a grouped product: same format, Hadamard and rotation.
+int check_operands(const qfp4_tensor* A, const qfp4_tensor* B) {
+    if (A == nullptr || B == nullptr) return QFP4_ERR_INVALID_ARG;
+    if (A->fmt != B->fmt || (A->fmt != QFP4_NVFP4 && A->fmt != QFP4_MXFP4)) return QFP4_ERR_INVALID_ARG;
+    if (A->had != B->had) return QFP4_ERR_INVALID_ARG;
+    if (had_random(A->had) && (A->rot_seed != B->rot_seed || A->rot_stream != B->rot_stream))
+        return QFP4_ERR_INVALID_ARG;
+    for (const qfp4_tensor* t : {A, B}) {
+        if (t->rows < 0 || t->k < 0 || t->rows > 0x7fffffffLL || t->k > 0x7fffffffLL) return QFP4_ERR_INVALID_ARG;
+        if (t->rows == 0 || t->k == 0) continue;
+        if (!t->codes || !t->scales || !t->tensor_scale) return QFP4_ERR_INVALID_ARG;
+        if (!aligned16(t->codes) || !aligned16(t->scales)) return QFP4_ERR_MISALIGNED;
+    }
+    return QFP4_OK;
+}
+
+// Tensor maps and launch of a grouped product (both directions); D has
+// d_rows rows of p.N columns.
+int run_grouped(const qfp4_tensor* A, const qfp4_tensor* B, bool wgrad, int64_t d_rows, GroupedParams& p, int sms,
+                cudaStream_t s) {
+    const int NB = block_of(A->fmt), apk = kGemmBK / (4 * NB);
+    const auto atoms_k = [&](int64_t k) { return (k / NB + 3) / 4; };
+    p.ga = A->tensor_scale;
+    p.gb = B->tensor_scale;
+    CUtensorMap tA, tB, tSFA, tSFB, tD;
+    int rc;
+    if ((rc = make_codes_tmap(&tA, A->codes, A->rows, A->k, kGemmBM))) return rc;
+    if ((rc = make_codes_tmap(&tB, B->codes, B->rows, B->k, 128))) return rc;
+    if ((rc = make_scale_tmap(&tSFA, A->scales, A->rows, atoms_k(A->k), apk, 1))) return rc;
+    if ((rc = make_scale_tmap(&tSFB, B->scales, B->rows, atoms_k(B->k), apk, 2))) return rc;
+    if ((rc = make_out_tmap(&tD, p.D, d_rows, p.N, p.ldd, p.out_f32))) return rc;
+    const cudaError_t e = launch_gemm_grouped(p, A->fmt, wgrad, &tA, &tB, &tSFA, &tSFB, &tD, s, sms);
+    return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
+}
+
+int gemm_grouped_impl(const qfp4_tensor* A, const qfp4_tensor* B, const int32_t* offsets, int32_t E, int64_t T, void* D,
+                      int64_t ldd, int32_t out_dtype, cudaStream_t s) {
+    int sms = 0, rc;
+    if ((rc = check_groups(offsets, E, T))) return rc;
+    if ((rc = check_operands(A, B))) return rc;
+    if (out_dtype != QFP4_OUT_BF16 && out_dtype != QFP4_OUT_F32) return QFP4_ERR_INVALID_ARG;
+    const int64_t K = A->k;
+    if (A->rows != group_rows(T, E) || K <= 0 || K % 64 != 0) return QFP4_ERR_INVALID_ARG;
+    // each group's part of B: along its rows, or along the reduction axis
+    const bool by_rows = B->k == K;
+    const int64_t N = by_rows ? B->rows / E : B->rows;
+    if (by_rows ? B->rows % E != 0 : B->k != K * E) return QFP4_ERR_INVALID_ARG;
+    if (N % 8 != 0 || (E > 1 && (by_rows ? N : K) % 128 != 0)) return QFP4_ERR_INVALID_ARG;
+    if ((T / 256 + E) * ((N + kGemmBN - 1) / kGemmBN) > 0x7fffffffLL) return QFP4_ERR_INVALID_ARG;
+    if (T == 0 || N == 0) return QFP4_OK;
+    const int64_t esz = out_dtype == QFP4_OUT_F32 ? 4 : 2;
+    if (D == nullptr || ldd < N) return QFP4_ERR_INVALID_ARG;
+    if (!aligned16(D) || (ldd * esz) % 16 != 0) return QFP4_ERR_MISALIGNED;
+    if ((rc = bind_context(s))) return rc;
+    if ((rc = check_device(&sms))) return rc;
+    GroupedParams p{};
+    p.offsets = offsets;
+    p.E = E; p.T = (int)T; p.Tp = (int)A->rows;
+    p.D = D;
+    p.ldd = ldd;
+    p.out_f32 = out_dtype == QFP4_OUT_F32;
+    p.N = (int)N; p.K = (int)K;
+    p.b_rows = by_rows ? (int)N : 0;
+    p.b_k = by_rows ? 0 : (int)K;
+    return run_grouped(A, B, false, T, p, sms, s);
+}
+
+int gemm_grouped_wgrad_impl(const qfp4_tensor* A, const qfp4_tensor* B, const int32_t* offsets, int32_t E, int64_t T,
+                            void* D, int32_t out_dtype, bool accumulate, cudaStream_t s) {
+    int sms = 0, rc;
+    if ((rc = check_groups(offsets, E, T))) return rc;
+    if ((rc = check_operands(A, B))) return rc;
+    if (out_dtype != QFP4_OUT_BF16 && out_dtype != QFP4_OUT_F32) return QFP4_ERR_INVALID_ARG;
+    if (accumulate && out_dtype != QFP4_OUT_F32) return QFP4_ERR_INVALID_ARG;
+    const int64_t M = A->rows, N = B->rows, Tp = group_rows(T, E);
+    if (A->k != Tp || B->k != Tp || M % 128 != 0 || N % 8 != 0) return QFP4_ERR_INVALID_ARG;
+    if (M * E > 0x7fffffffLL || E * ((M + 255) / 256) * ((N + kGemmBN - 1) / kGemmBN) > 0x7fffffffLL)
+        return QFP4_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return QFP4_OK;
+    if (D == nullptr) return QFP4_ERR_INVALID_ARG;
+    if (!aligned16(D)) return QFP4_ERR_MISALIGNED;
+    const size_t esz = out_dtype == QFP4_OUT_F32 ? 4 : 2;
+    if ((rc = bind_context(s))) return rc;
+    if ((rc = check_device(&sms))) return rc;
+    if (T == 0) {
+        if (accumulate) return QFP4_OK;
+        const cudaError_t e = cudaMemsetAsync(D, 0, (size_t)(M * N) * E * esz, s);
+        return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
+    }
+    GroupedParams p{};
+    p.offsets = offsets;
+    p.E = E; p.T = (int)T; p.Tp = (int)Tp;
+    p.D = D;
+    p.ldd = N;
+    p.out_f32 = out_dtype == QFP4_OUT_F32;
+    p.accumulate = accumulate ? 1 : 0;
+    p.M = (int)M; p.N = (int)N;
+    return run_grouped(A, B, true, M * E, p, sms, s);
+}
+
+// xp = x in the padded layout.
+int group_pad(const void* x, int64_t T, int64_t C, int64_t ld, const int32_t* offsets, int32_t E, void* xp,
+              cudaStream_t s) {
+    int sms = 0;
+    int rc = bind_context(s);
+    if (rc) return rc;
+    if ((rc = check_device(&sms))) return rc;
+    if (T == 0 || C == 0) return QFP4_OK;
+    const cudaError_t e = launch_group_pad(x, ld, C, offsets, E, (int)T, (int)group_rows(T, E), xp, sms, s);
+    return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
+}
+
+int quantize_grouped_impl(const void* x, int64_t T, int64_t C, int64_t ld, const int32_t* offsets, int32_t E,
+                          int32_t fmt, int32_t rounding, int32_t had, int32_t axis, const qfp4_seed* seed,
+                          const float* amax_in, qfp4_tensor* out, void* workspace, size_t workspace_bytes,
+                          cudaStream_t s) {
+    int rc = check_groups(offsets, E, T);
+    if (rc) return rc;
+    Geometry g;
+    if ((rc = validate_input(x, T, C, ld, QFP4_HAD_NONE, axis, &g))) return rc;
+    if (!valid_fmt(fmt) || rounding < QFP4_RTN || rounding > QFP4_QUARTET2 || had < QFP4_HAD_NONE ||
+        had > QFP4_HAD_RAND32)
+        return QFP4_ERR_INVALID_ARG;
+    const int64_t unit = std::max(block_of(fmt), had_n(had));
+    if (C % 8 != 0 || (axis == QFP4_AXIS_ROW && C % unit != 0)) return QFP4_ERR_INVALID_ARG;
+    if (out == nullptr || out->tensor_scale == nullptr || seed == nullptr || seed->rot_stream >= (1u << 28) ||
+        seed->sr_stream >= (1u << 28))
+        return QFP4_ERR_INVALID_ARG;
+    if (T > 0 && C > 0) {
+        if (out->codes == nullptr || out->scales == nullptr) return QFP4_ERR_INVALID_ARG;
+        if (!aligned16(out->codes) || !aligned16(out->scales)) return QFP4_ERR_MISALIGNED;
+    }
+    if (workspace == nullptr || workspace_bytes < qfp4_quantize_grouped_workspace_bytes(T, C, E))
+        return QFP4_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return QFP4_ERR_MISALIGNED;
+    Carver c{static_cast<uint8_t*>(workspace), 0};
+    void* partials = c.take(qfp4_quantize_workspace_bytes());
+    const int64_t Tp = group_rows(T, E);
+    void* xp = c.take((size_t)(Tp * C) * 2);
+    if ((rc = group_pad(x, T, C, ld, offsets, E, xp, s))) return rc;
+    return quantize_impl(xp, Tp, C, C, fmt, rounding, had, axis, seed, amax_in, out, partials,
+                         qfp4_quantize_workspace_bytes(), s);
+}
+
+// ---- linear layer of a mixture of experts -----------------------------------------
+int check_linear_grouped(const int32_t* offsets, int32_t E, int64_t T, int64_t N, int64_t K, const qfp4_recipe* r,
+                         const qfp4_seed* seed) {
+    const int rc = check_groups(offsets, E, T);
+    if (rc) return rc;
+    return check_linear_args(128, N * E, K, r, seed) || N % 128 != 0 || N * E > 0x7fffffffLL || K * E > 0x7fffffffLL
+               ? QFP4_ERR_INVALID_ARG
+               : QFP4_OK;
+}
+
+struct GroupedLayout {
+    float* partials;
+    float* dy_amax;
+    void* xp;       // X in the padded layout
+    void* dyp;      // dY in the padded layout
+    qfp4_tensor t[4];
+    size_t total;
+};
+GroupedLayout grouped_layout(int backward, int64_t T, int32_t E, int64_t N, int64_t K, const qfp4_recipe* r,
+                             uint8_t* ws) {
+    GroupedLayout l{};
+    Carver c{ws, 0};
+    const int64_t Tp = group_rows(T, E);
+    l.partials = static_cast<float*>(c.take(qfp4_quantize_workspace_bytes()));
+    l.xp = c.take((size_t)(Tp * K) * 2);
+    if (!backward) {
+        carve_operand(c, &l.t[0], r->fprop.fmt, Tp, K);     // X along K
+        carve_operand(c, &l.t[1], r->fprop.fmt, N * E, K);  // W along K
+    } else {
+        l.dy_amax = static_cast<float*>(c.take(2 * sizeof(float)));
+        l.dyp = c.take((size_t)(Tp * N) * 2);
+        carve_operand(c, &l.t[0], r->dgrad.fmt, Tp, N);     // dY along N
+        carve_operand(c, &l.t[1], r->dgrad.fmt, K, N * E);  // W^T: W along N
+        carve_operand(c, &l.t[2], r->wgrad.fmt, N, Tp);     // dY^T: dY along the tokens
+        carve_operand(c, &l.t[3], r->wgrad.fmt, K, Tp);     // X^T: X along the tokens
+    }
+    l.total = c.off;
+    return l;
+}
+}  // namespace
+}  // namespace qfp4
+
+extern "C" {
+
+int qfp4_rmsnorm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* w, int64_t R, int64_t C,
+                     float eps, void* h, int64_t ldh, void* y, int64_t ldy, float* rstd, int32_t had,
+                     const qfp4_seed* seed, float* y_amax, void* workspace, size_t workspace_bytes, void* stream) {
+    const ApiRange range("qfp4_rmsnorm_fwd");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int sms = 0, rc;
+    NormParams p{};
+    if ((rc = norm_fwd_args(x, ldx, res, ldres, w, R, C, eps, h, ldh, y, ldy, rstd, had, seed, &p))) return rc;
+    if (y == nullptr && R > 0) return QFP4_ERR_INVALID_ARG;
+    if (y_amax != nullptr) {
+        if (workspace == nullptr || workspace_bytes < qfp4_quantize_workspace_bytes()) return QFP4_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return QFP4_ERR_MISALIGNED;
+    }
+    if ((rc = bind_context(s))) return rc;
+    if ((rc = check_device(&sms))) return rc;
+    if (R == 0) return y_amax != nullptr ? set_zero(y_amax, 1, s) : QFP4_OK;
+    p.amax_out = static_cast<float*>(workspace);
+    int n = 0;
+    cudaError_t e = launch_rmsnorm_fwd(p, y_amax != nullptr ? had_n(had) : -1, false, y_amax, sms, &n, s);
+    if (e == cudaSuccess && y_amax != nullptr && n > 1)
+        e = launch_reduce_max(static_cast<const float*>(workspace), n, y_amax, s);
+    return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
+}
+
+int qfp4_rmsnorm_quantize(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* w, int64_t R,
+                          int64_t C, float eps, void* h, int64_t ldh, void* y, int64_t ldy, float* rstd, int32_t fmt,
+                          int32_t had, const qfp4_seed* seed, qfp4_tensor* out, void* stream) {
+    const ApiRange range("qfp4_rmsnorm_quantize");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int sms = 0, rc;
+    NormParams p{};
+    if ((rc = norm_fwd_args(x, ldx, res, ldres, w, R, C, eps, h, ldh, y, ldy, rstd, had, seed, &p))) return rc;
+    if ((fmt != QFP4_MXFP4 && fmt != QFP4_MXFP4_RU) || C % 32 != 0) return QFP4_ERR_INVALID_ARG;
+    if (out == nullptr || out->tensor_scale == nullptr) return QFP4_ERR_INVALID_ARG;
+    if (R > 0) {
+        if (out->codes == nullptr || out->scales == nullptr) return QFP4_ERR_INVALID_ARG;
+        if (!aligned16(out->codes) || !aligned16(out->scales)) return QFP4_ERR_MISALIGNED;
+    }
+    if ((rc = bind_context(s))) return rc;
+    if ((rc = check_device(&sms))) return rc;
+    fill_out(out, R, C, fmt, had, seed);
+    if (R == 0) return write_one(out->tensor_scale, s);
+    p.q_codes = out->codes;
+    p.q_scales = out->scales;
+    p.q_tensor_scale = out->tensor_scale;
+    p.q_kb4 = (C / 32 + 3) / 4 * 4;
+    p.q_round_up = fmt == QFP4_MXFP4_RU ? 1u : 0u;
+    const cudaError_t e = launch_rmsnorm_fwd(p, had_n(had), true, nullptr, sms, nullptr, s);
+    return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
+}
+
+size_t qfp4_rmsnorm_bwd_workspace_bytes(int64_t R, int64_t C) {
+    if (R <= 0 || C <= 0) return 0;
+    return (size_t)(norm_bwd_partial_rows(R) * C) * sizeof(float);
+}
+
+int qfp4_rmsnorm_bwd(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* w, const float* rstd,
+                     const void* dh, int64_t lddh, int64_t R, int64_t C, void* dx, int64_t lddx, float* dw,
+                     int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+    const ApiRange range("qfp4_rmsnorm_bwd");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int sms = 0, rc;
+    if ((rc = check_norm(w, R, C))) return rc;
+    if ((rc = check_matrix(dy, R, C, lddy))) return rc;
+    if ((rc = check_matrix(h, R, C, ldh))) return rc;
+    if (dh != nullptr && (rc = check_matrix(dh, R, C, lddh))) return rc;
+    if ((rc = check_matrix(dx, R, C, lddx))) return rc;
+    if (dw == nullptr || (R > 0 && rstd == nullptr) || (accumulate != 0 && accumulate != 1))
+        return QFP4_ERR_INVALID_ARG;
+    if (R > 0) {
+        if (workspace == nullptr || workspace_bytes < qfp4_rmsnorm_bwd_workspace_bytes(R, C))
+            return QFP4_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return QFP4_ERR_MISALIGNED;
+    }
+    if ((rc = bind_context(s))) return rc;
+    if ((rc = check_device(&sms))) return rc;
+    if (R == 0) return accumulate ? QFP4_OK : set_zero(dw, C, s);
+    NormBwdParams p{};
+    p.dy = static_cast<const uint16_t*>(dy);
+    p.h = static_cast<const uint16_t*>(h);
+    p.w = static_cast<const uint16_t*>(w);
+    p.rstd = rstd;
+    p.dh = static_cast<const uint16_t*>(dh);
+    p.lddy = lddy; p.ldh = ldh; p.lddh = lddh; p.R = R; p.C = C;
+    p.inv_c = 1.0f / (float)C;
+    p.dx = static_cast<uint16_t*>(dx);
+    p.lddx = lddx;
+    p.dw_partials = static_cast<float*>(workspace);
+    const cudaError_t e = launch_rmsnorm_bwd(p, dw, accumulate, sms, s);
+    return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
+}
+
+int64_t qfp4_group_rows(int64_t T, int32_t E) {
+    return E < 1 || E > QFP4_MAX_GROUPS || T < 0 ? -1 : group_rows(T, E);
+}
+
+size_t qfp4_quantize_grouped_workspace_bytes(int64_t T, int64_t C, int32_t E) {
+    if (T < 0 || C < 0 || E < 1 || E > QFP4_MAX_GROUPS) return 0;
+    Carver c{nullptr, 0};
+    c.take(qfp4_quantize_workspace_bytes());
+    c.take((size_t)(group_rows(T, E) * C) * 2);
+    return c.off;
+}
+
+int qfp4_quantize_grouped(const void* x, int64_t T, int64_t C, int64_t ld, const int32_t* offsets, int32_t E,
+                          int32_t fmt, int32_t rounding, int32_t had, int32_t axis, const qfp4_seed* seed,
+                          const float* amax_in, qfp4_tensor* out, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+    const ApiRange range("qfp4_quantize_grouped");
+    return quantize_grouped_impl(x, T, C, ld, offsets, E, fmt, rounding, had, axis, seed, amax_in, out, workspace,
+                                 workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+int qfp4_gemm_grouped(const qfp4_tensor* A, const qfp4_tensor* B, const int32_t* offsets, int32_t E, int64_t T, void* D,
+                      int64_t ldd, int32_t out_dtype, void* stream) {
+    const ApiRange range("qfp4_gemm_grouped");
+    return gemm_grouped_impl(A, B, offsets, E, T, D, ldd, out_dtype, static_cast<cudaStream_t>(stream));
+}
+
+int qfp4_gemm_grouped_wgrad(const qfp4_tensor* A, const qfp4_tensor* B, const int32_t* offsets, int32_t E, int64_t T,
+                            void* D, int32_t out_dtype, int32_t accumulate, void* stream) {
+    const ApiRange range("qfp4_gemm_grouped_wgrad");
+    if (accumulate != 0 && accumulate != 1) return QFP4_ERR_INVALID_ARG;
+    return gemm_grouped_wgrad_impl(A, B, offsets, E, T, D, out_dtype, accumulate != 0,
+                                   static_cast<cudaStream_t>(stream));
+}
+
+size_t qfp4_linear_grouped_workspace_bytes(int32_t backward, int64_t T, int32_t E, int64_t N, int64_t K,
+                                           const qfp4_recipe* recipe) {
+    if (recipe == nullptr || T < 0 || N < 0 || K < 0 || E < 1 || E > QFP4_MAX_GROUPS) return 0;
+    return grouped_layout(backward, T, E, N, K, recipe, nullptr).total;
+}
+
+int qfp4_linear_grouped_fwd(const void* X, const void* W, void* Y, const int32_t* offsets, int32_t E, int64_t T,
+                            int64_t N, int64_t K, const qfp4_recipe* recipe, const qfp4_seed* seed,
+                            const float* x_amax, void* workspace, size_t workspace_bytes, void* stream) {
+    const ApiRange range("qfp4_linear_grouped_fwd");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int rc = check_linear_grouped(offsets, E, T, N, K, recipe, seed);
+    if (rc) return rc;
+    if (!W || (T > 0 && (!X || !Y))) return QFP4_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(W) || !aligned16(Y)) return QFP4_ERR_MISALIGNED;
+    if (workspace == nullptr || workspace_bytes < qfp4_linear_grouped_workspace_bytes(0, T, E, N, K, recipe))
+        return QFP4_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return QFP4_ERR_MISALIGNED;
+    if (T == 0) return QFP4_OK;
+    GroupedLayout l = grouped_layout(0, T, E, N, K, recipe, static_cast<uint8_t*>(workspace));
+    const qfp4_gemm_cfg& c = recipe->fprop;
+    const size_t pws = qfp4_quantize_workspace_bytes();
+    const int64_t Tp = group_rows(T, E);
+    const qfp4_seed sx = op_seed(seed, 0, 0), sw = op_seed(seed, 0, 1);
+    const float* ax = c.fmt == QFP4_NVFP4 ? x_amax : nullptr;
+    if ((rc = group_pad(X, T, K, K, offsets, E, l.xp, s))) return rc;
+    if ((rc = quantize_impl(l.xp, Tp, K, K, c.fmt, c.rnd_a, c.had, QFP4_AXIS_ROW, &sx, ax, &l.t[0], l.partials, pws,
+                            s)))
+        return rc;
+    if ((rc = quantize_impl(W, N * E, K, K, c.fmt, c.rnd_b, c.had, QFP4_AXIS_ROW, &sw, nullptr, &l.t[1], l.partials,
+                            pws, s)))
+        return rc;
+    return gemm_grouped_impl(&l.t[0], &l.t[1], offsets, E, T, Y, N, recipe->y_dtype, s);
+}
+
+int qfp4_linear_grouped_bwd(const void* dY, const void* X, const void* W, void* dX, void* dW, const int32_t* offsets,
+                            int32_t E, int64_t T, int64_t N, int64_t K, const qfp4_recipe* recipe,
+                            const qfp4_seed* seed, void* workspace, size_t workspace_bytes, void* stream) {
+    const ApiRange range("qfp4_linear_grouped_bwd");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int rc = check_linear_grouped(offsets, E, T, N, K, recipe, seed);
+    if (rc) return rc;
+    if (!W || !dW || (T > 0 && (!dY || !X || !dX))) return QFP4_ERR_INVALID_ARG;
+    if (!aligned16(dY) || !aligned16(X) || !aligned16(W) || !aligned16(dX) || !aligned16(dW)) return QFP4_ERR_MISALIGNED;
+    if (workspace == nullptr || workspace_bytes < qfp4_linear_grouped_workspace_bytes(1, T, E, N, K, recipe))
+        return QFP4_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return QFP4_ERR_MISALIGNED;
+    const bool dw_add = recipe->dw_accumulate != 0;
+    if (T == 0) {  // no rows: dW = 0
+        if ((rc = bind_context(s))) return rc;
+        if (dw_add) return QFP4_OK;
+        const size_t esz = recipe->dw_dtype == QFP4_OUT_F32 ? 4 : 2;
+        const cudaError_t e = cudaMemsetAsync(dW, 0, (size_t)(N * K) * E * esz, s);
+        return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
+    }
+    GroupedLayout l = grouped_layout(1, T, E, N, K, recipe, static_cast<uint8_t*>(workspace));
+    const size_t pws = qfp4_quantize_workspace_bytes();
+    const int64_t Tp = group_rows(T, E);
+    const qfp4_gemm_cfg& d = recipe->dgrad;
+    const qfp4_gemm_cfg& w = recipe->wgrad;
+    const qfp4_seed s1 = op_seed(seed, 1, 3), s2 = op_seed(seed, 2, 4), s3 = op_seed(seed, 2, 5);
+    bool dy_done;
+    const float* dy_am_col;
+    if ((rc = group_pad(dY, T, N, N, offsets, E, l.dyp, s))) return rc;
+    if ((rc = quantize_dy(l.dyp, Tp, N, recipe, seed, &l.t[0], &l.t[2], l.dy_amax, l.partials, &dy_done, &dy_am_col, s)))
+        return rc;
+    // Dgrad dX[e] = dY[e] . W[e]: reduce over N, W's experts along the reduction axis.
+    if ((rc = quantize_impl(W, N * E, K, K, d.fmt, d.rnd_b, d.had, QFP4_AXIS_COL, &s1, nullptr, &l.t[1], l.partials, pws,
+                            s)))
+        return rc;
+    if ((rc = gemm_grouped_impl(&l.t[0], &l.t[1], offsets, E, T, dX, K, recipe->dx_dtype, s))) return rc;
+    // Wgrad dW[e] = dY[e]^T . X[e]: reduce over the group's tokens.
+    if (!dy_done && (rc = quantize_impl(l.dyp, Tp, N, N, w.fmt, w.rnd_a, w.had, QFP4_AXIS_COL, &s2, dy_am_col, &l.t[2],
+                                        l.partials, pws, s)))
+        return rc;
+    if ((rc = group_pad(X, T, K, K, offsets, E, l.xp, s))) return rc;
+    if ((rc = quantize_impl(l.xp, Tp, K, K, w.fmt, w.rnd_b, w.had, QFP4_AXIS_COL, &s3, nullptr, &l.t[3], l.partials, pws,
+                            s)))
+        return rc;
+    return gemm_grouped_wgrad_impl(&l.t[2], &l.t[3], offsets, E, T, dW, recipe->dw_dtype, dw_add, s);
 }
 
 int qfp4_status(void* stream) {
@@ -1080,7 +1557,7 @@ int qfp4_status(void* stream) {
     if (v != 0) {
         const uint32_t zero = 0;
         if ((e = cudaMemcpyToSymbol(g_dev_error, &zero, sizeof zero)) != cudaSuccess) return cuda_fail(e);
-        return (v & DEV_ERR_BOUNDS) ? QFP4_ERR_BOUNDS : QFP4_ERR_TIMEOUT;
+        return (v & DEV_ERR_BOUNDS) ? QFP4_ERR_BOUNDS : (v & DEV_ERR_TIMEOUT) ? QFP4_ERR_TIMEOUT : QFP4_ERR_OFFSETS;
     }
     return QFP4_OK;
 }

@@ -16,7 +16,8 @@ namespace qfp4 {
 // ---------------------------------------------------------------------------
 // error word: set by a kernel whose bounded wait expired; read by qfp4_status()
 // DEV_ERR_BOUNDS: a bounds-checked build caught a store outside its buffer
-enum : uint32_t { DEV_ERR_NONE = 0, DEV_ERR_TIMEOUT = 1, DEV_ERR_BOUNDS = 2 };
+// DEV_ERR_OFFSETS: group offsets that fall or leave their rows
+enum : uint32_t { DEV_ERR_NONE = 0, DEV_ERR_TIMEOUT = 1, DEV_ERR_BOUNDS = 2, DEV_ERR_OFFSETS = 4 };
 // (the library is one translation unit, see qfp4_lib.cu, so this is its only definition)
 __device__ uint32_t g_dev_error = 0;
 

@@ -132,6 +132,76 @@ cudaError_t launch_gemm_pair(const GemmParams& p, int fmt, const CUtensorMap* tm
                              cudaStream_t s, int sms, int nhq = -1, int amx = -1, int* n_partials = nullptr);
 constexpr int kGemmBM = 128, kGemmBN = 256, kGemmBK = 256;
 
+// norm.cu: RMSNorm forward and backward
+struct NormParams {
+    const uint16_t* x;    // bf16 R x C, row stride ldx
+    const uint16_t* res;  // nullable
+    const uint16_t* w;    // bf16 [C]
+    int64_t ldx, ldres, R, C;
+    double eps, inv_c;    // inv_c = 1 / C
+    uint16_t* h;          // nullable without res
+    uint16_t* y;          // nullable with the quantized output
+    int64_t ldh, ldy;
+    float* rstd;
+    float* amax_out;      // one partial maximum per CTA
+    uint32_t signs;       // random Hadamard sign bits (0 for deterministic / none)
+    // the MXFP4 quantization of y along its rows
+    uint8_t* q_codes;
+    uint8_t* q_scales;
+    float* q_tensor_scale;
+    int64_t q_kb4;
+    uint32_t q_round_up;
+};
+struct NormBwdParams {
+    const uint16_t* dy;
+    const uint16_t* h;
+    const uint16_t* w;
+    const float* rstd;
+    const uint16_t* dh;  // nullable
+    int64_t lddy, ldh, lddh, R, C;
+    float inv_c;
+    uint16_t* dx;
+    int64_t lddx;
+    float* dw_partials;  // one row of C per row owner
+};
+// At most this many rows of weight-gradient partials (four row owners per SM).
+constexpr int kMaxNormPartials = 592;
+// nh: -1 no amax, else the Hadamard size of the amax or of the quantization;
+// *n_partials receives the number of partial maxima; a single one goes to
+// *amax instead of p.amax_out.
+cudaError_t launch_rmsnorm_fwd(NormParams p, int nh, bool quant, float* amax, int sms, int* n_partials,
+                               cudaStream_t s);
+int64_t norm_bwd_partial_rows(int64_t R);
+cudaError_t launch_rmsnorm_bwd(const NormBwdParams& p, float* dw, int accumulate, int sms, cudaStream_t s);
+
+// grouped_sm100.cu: rows in groups (the experts of a mixture). offsets: device
+// int32 [E + 1], group e's rows are [offsets[e], offsets[e + 1]) of T; in the
+// padded layout it starts at row sum_{i<e} 128 ceil(m_i / 128) of Tp.
+constexpr int kMaxGroups = 256;
+struct GroupedParams {
+    const int* offsets;
+    int E, T, Tp;
+    const float* ga;
+    const float* gb;
+    void* D;
+    int64_t ldd;
+    int out_f32;
+    int accumulate;
+    // M: rows of A per group (weight gradient only); N: columns of D; K: the
+    // reduction length (rows mode only); group e's part of B starts at row
+    // e * b_rows and at element e * b_k of the reduction axis
+    int M, N, K;
+    int b_rows, b_k;
+};
+// wgrad: the reduction runs over the groups' rows (D [E M x N]); else over K,
+// with the groups along the rows of A and D.
+cudaError_t launch_gemm_grouped(const GroupedParams& p, int fmt, bool wgrad, const CUtensorMap* tmapA,
+                                const CUtensorMap* tmapB, const CUtensorMap* tmapSFA, const CUtensorMap* tmapSFB,
+                                const CUtensorMap* tmapD, cudaStream_t s, int sms);
+// xp [Tp x C] (contiguous) = the groups' rows of x in the padded layout, zeros elsewhere.
+cudaError_t launch_group_pad(const void* x, int64_t ld, int64_t C, const int* offsets, int E, int T, int Tp, void* xp,
+                             int sms, cudaStream_t s);
+
 void count_launch();
 
 }  // namespace qfp4

@@ -29,6 +29,7 @@ BLOCK = {NVFP4: 16, MXFP4: 32, MXFP4_RU: 32}
 OK, ERR_INVALID_ARG, ERR_MISALIGNED, ERR_UNSUPPORTED_ARCH, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT = 0, -1, -2, -3, -4, -5, -6
 ERR_TOO_LARGE = -7
 ERR_BOUNDS = -8
+ERR_OFFSETS = -9
 NOALLOC_SCRATCH_BYTES = 32 << 20
 ROUND_E2M1_SR, ROUND_E2M1_RN, ROUND_E4M3_SR, ROUND_E4M3_RN, ROUND_E8M0_SR = 0, 1, 2, 3, 4
 
@@ -64,6 +65,7 @@ class QFP4Error(RuntimeError):
 
 _lib = None
 _VOID, _I32, _I64, _U64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_size_t
+_F32 = ctypes.c_float
 
 _SIGNATURES = {
     "qfp4_strerror": (ctypes.c_char_p, [ctypes.c_int]),
@@ -98,6 +100,28 @@ _SIGNATURES = {
                                              _SZ, _VOID]),
     "qfp4_linear_fwd_noalloc": (ctypes.c_int, [_VOID, _VOID, _VOID, _I64, _I64, _I64, ctypes.POINTER(Recipe),
                                                ctypes.POINTER(Seed), _VOID]),
+    "qfp4_rmsnorm_fwd": (ctypes.c_int, [_VOID, _I64, _VOID, _I64, _VOID, _I64, _I64, _F32, _VOID, _I64, _VOID, _I64,
+                                        _VOID, _I32, ctypes.POINTER(Seed), _VOID, _VOID, _SZ, _VOID]),
+    "qfp4_rmsnorm_quantize": (ctypes.c_int, [_VOID, _I64, _VOID, _I64, _VOID, _I64, _I64, _F32, _VOID, _I64, _VOID,
+                                             _I64, _VOID, _I32, _I32, ctypes.POINTER(Seed), ctypes.POINTER(TensorDesc),
+                                             _VOID]),
+    "qfp4_rmsnorm_bwd_workspace_bytes": (_SZ, [_I64, _I64]),
+    "qfp4_rmsnorm_bwd": (ctypes.c_int, [_VOID, _I64, _VOID, _I64, _VOID, _VOID, _VOID, _I64, _I64, _I64, _VOID, _I64,
+                                        _VOID, _I32, _VOID, _SZ, _VOID]),
+    "qfp4_group_rows": (_I64, [_I64, _I32]),
+    "qfp4_quantize_grouped_workspace_bytes": (_SZ, [_I64, _I64, _I32]),
+    "qfp4_quantize_grouped": (ctypes.c_int, [_VOID, _I64, _I64, _I64, _VOID, _I32, _I32, _I32, _I32, _I32,
+                                             ctypes.POINTER(Seed), _VOID, ctypes.POINTER(TensorDesc), _VOID, _SZ,
+                                             _VOID]),
+    "qfp4_gemm_grouped": (ctypes.c_int, [ctypes.POINTER(TensorDesc), ctypes.POINTER(TensorDesc), _VOID, _I32, _I64,
+                                         _VOID, _I64, _I32, _VOID]),
+    "qfp4_gemm_grouped_wgrad": (ctypes.c_int, [ctypes.POINTER(TensorDesc), ctypes.POINTER(TensorDesc), _VOID, _I32,
+                                               _I64, _VOID, _I32, _I32, _VOID]),
+    "qfp4_linear_grouped_workspace_bytes": (_SZ, [_I32, _I64, _I32, _I64, _I64, ctypes.POINTER(Recipe)]),
+    "qfp4_linear_grouped_fwd": (ctypes.c_int, [_VOID, _VOID, _VOID, _VOID, _I32, _I64, _I64, _I64,
+                                               ctypes.POINTER(Recipe), ctypes.POINTER(Seed), _VOID, _VOID, _SZ, _VOID]),
+    "qfp4_linear_grouped_bwd": (ctypes.c_int, [_VOID, _VOID, _VOID, _VOID, _VOID, _VOID, _I32, _I64, _I64, _I64,
+                                               ctypes.POINTER(Recipe), ctypes.POINTER(Seed), _VOID, _SZ, _VOID]),
     "qfp4_status": (ctypes.c_int, [_VOID]),
     "qfp4_selftest_wait_timeout": (ctypes.c_int, [_I64, _VOID]),
     "qfp4_selftest_rounding": (ctypes.c_int, [_I32, _VOID, _VOID, _VOID, _I64, _VOID]),
@@ -373,6 +397,210 @@ def linear_bwd(dY, X, W, rec: Recipe, seed: Seed, dX=None, dW=None, workspace=No
     return dX, dW
 
 
+# ---------------------------------------------------------------------------
+# RMSNorm
+
+def _matrix(t: torch.Tensor, like: torch.Tensor | None = None, dtype=torch.bfloat16) -> torch.Tensor:
+    """Check a 2-D tensor with contiguous rows (of `like`'s shape and device)."""
+    assert t.dtype == dtype and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1)
+    assert like is None or (t.shape == like.shape and t.device == like.device)
+    return t
+
+
+def _ld(t: torch.Tensor | None) -> int:
+    """Row stride of a matrix (a single row's is not looked at)."""
+    if t is None:
+        return 0
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 8)
+
+
+def _norm_outputs(x, w, res, y, h, rstd, want_y=True):
+    R, C = _matrix(x).shape
+    assert w.dtype == torch.bfloat16 and w.shape == (C,) and w.is_contiguous() and w.device == x.device
+    assert res is None or _matrix(res, x) is res
+    if want_y:
+        y = torch.empty((R, C), dtype=torch.bfloat16, device=x.device) if y is None else _matrix(y, x)
+    if res is None:
+        h = x if h is None else _matrix(h, x)
+    else:
+        h = torch.empty((R, C), dtype=torch.bfloat16, device=x.device) if h is None else _matrix(h, x)
+    if rstd is None:
+        rstd = torch.empty((R,), dtype=torch.float32, device=x.device)
+    assert rstd.dtype == torch.float32 and rstd.shape == (R,) and rstd.is_contiguous() and rstd.device == x.device
+    return y, h, rstd
+
+
+def rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, eps: float, res: torch.Tensor | None = None, had: int = HAD_NONE,
+                seed: Seed | None = None, want_amax: bool = False, y=None, h=None, rstd=None, y_amax=None,
+                workspace=None, stream=None):
+    """h = x + res, y = h / rms(h) * w; see qfp4_rmsnorm_fwd. Returns (y, h,
+    rstd, y_amax): without res, h is x itself unless a buffer for it is given;
+    y_amax, y's NVFP4 tensor amax after the rotation `had`, is None unless
+    wanted (want_amax or a buffer for it)."""
+    y, h, rstd = _norm_outputs(x, w, res, y, h, rstd)
+    if want_amax and y_amax is None:
+        y_amax = torch.empty((1,), dtype=torch.float32, device=x.device)
+    if y_amax is not None and workspace is None:
+        workspace = torch.empty((quantize_workspace_bytes(),), dtype=torch.uint8, device=x.device)
+    hp = None if res is None and h is x else h
+    _check(lib().qfp4_rmsnorm_fwd(_ptr(x), _ld(x), _ptr(res), _ld(res), _ptr(w), *x.shape, eps, _ptr(hp), _ld(hp),
+                                  _ptr(y), _ld(y), _ptr(rstd), had, None if seed is None else ctypes.byref(seed),
+                                  _ptr(y_amax), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                  _stream(stream)), "qfp4_rmsnorm_fwd")
+    return y, h, rstd, y_amax
+
+
+def rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, eps: float, res: torch.Tensor | None = None, fmt: int = MXFP4,
+                     had: int = HAD_NONE, seed: Seed | None = None, want_y: bool = True, y=None, h=None, rstd=None,
+                     out: QTensor | None = None, stream=None):
+    """rmsnorm_fwd and y's MXFP4 (or MXFP4_RU) quantization along its rows; see
+    qfp4_rmsnorm_quantize. Returns (y, h, rstd, q); y is None unless wanted."""
+    y, h, rstd = _norm_outputs(x, w, res, y, h, rstd, want_y or y is not None)
+    out = empty_qtensor(MXFP4, x.shape[0], x.shape[1], x.device) if out is None else out
+    hp = None if res is None and h is x else h
+    _check(lib().qfp4_rmsnorm_quantize(_ptr(x), _ld(x), _ptr(res), _ld(res), _ptr(w), *x.shape, eps, _ptr(hp), _ld(hp),
+                                       _ptr(y), _ld(y), _ptr(rstd), fmt, had,
+                                       None if seed is None else ctypes.byref(seed), ctypes.byref(out.desc),
+                                       _stream(stream)), "qfp4_rmsnorm_quantize")
+    return y, h, rstd, out
+
+
+def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: torch.Tensor, dh: torch.Tensor | None = None,
+                dx=None, dw=None, accumulate: bool = False, workspace=None, stream=None):
+    """Gradients (dx, dw) of rmsnorm_fwd from y's gradient and (dh) h's own;
+    see qfp4_rmsnorm_bwd. dx is the gradient of x and of res alike; dw is fp32."""
+    R, C = _matrix(dy).shape
+    _matrix(h, dy)
+    assert w.dtype == torch.bfloat16 and w.shape == (C,) and w.is_contiguous() and w.device == dy.device
+    assert rstd.dtype == torch.float32 and rstd.shape == (R,) and rstd.is_contiguous() and rstd.device == dy.device
+    assert dh is None or _matrix(dh, dy) is dh
+    dx = torch.empty((R, C), dtype=torch.bfloat16, device=dy.device) if dx is None else _matrix(dx, dy)
+    if accumulate and dw is None:
+        raise ValueError("accumulate adds into dw: pass the buffer")
+    dw = torch.empty((C,), dtype=torch.float32, device=dy.device) if dw is None else dw
+    assert dw.dtype == torch.float32 and dw.shape == (C,) and dw.is_contiguous() and dw.device == dy.device
+    if workspace is None:
+        workspace = torch.empty((lib().qfp4_rmsnorm_bwd_workspace_bytes(R, C),), dtype=torch.uint8, device=dy.device)
+    _check(lib().qfp4_rmsnorm_bwd(_ptr(dy), _ld(dy), _ptr(h), _ld(h), _ptr(w), _ptr(rstd), _ptr(dh), _ld(dh), R, C,
+                                  _ptr(dx), _ld(dx), _ptr(dw), 1 if accumulate else 0, _ptr(workspace),
+                                  workspace.numel(), _stream(stream)), "qfp4_rmsnorm_bwd")
+    return dx, dw
+
+
+# ---------------------------------------------------------------------------
+# groups of rows: the experts of a mixture
+
+def group_rows(T: int, E: int) -> int:
+    """Rows of the padded layout of T rows in E groups."""
+    return lib().qfp4_group_rows(T, E)
+
+
+def _groups(offsets: torch.Tensor, like: torch.Tensor) -> int:
+    """Check the group offsets (int32 [E + 1] on the tensors' device); E."""
+    assert offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.is_contiguous() and offsets.numel() >= 2
+    assert offsets.device == like.device
+    return offsets.numel() - 1
+
+
+def quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, fmt: int, rounding: int, had: int, axis: int,
+                     seed: Seed | None = None, amax_in: torch.Tensor | None = None, out: QTensor | None = None,
+                     workspace=None, stream=None) -> QTensor:
+    """Quantize rows sorted by group, in the padded layout; see qfp4_quantize_grouped."""
+    T, C = _matrix(x).shape
+    E = _groups(offsets, x)
+    Tp = group_rows(T, E)
+    rows, k = (Tp, C) if axis == ROW else (C, Tp)
+    out = empty_qtensor(fmt, max(rows, 0), max(k, 0), x.device) if out is None else out
+    if workspace is None:
+        workspace = torch.empty((lib().qfp4_quantize_grouped_workspace_bytes(T, C, E),), dtype=torch.uint8,
+                                device=x.device)
+    seed = seed or make_seed()
+    _check(lib().qfp4_quantize_grouped(_ptr(x), T, C, _ld(x), _ptr(offsets), E, fmt, rounding, had, axis,
+                                       ctypes.byref(seed), _ptr(amax_in), ctypes.byref(out.desc), _ptr(workspace),
+                                       workspace.numel(), _stream(stream)), "qfp4_quantize_grouped")
+    return out
+
+
+def gemm_grouped(A: QTensor, B: QTensor, offsets: torch.Tensor, T: int, out_dtype=torch.bfloat16,
+                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Each group's rows of A times its part of B, as T rows; see
+    qfp4_gemm_grouped. Rows of no group are not written."""
+    E = _groups(offsets, A.codes)
+    N = B.rows // E if B.k == A.k else B.rows
+    if out is None:
+        out = torch.empty((T, N), dtype=out_dtype, device=A.codes.device)
+    _matrix(out, dtype=out.dtype)
+    assert out.shape == (T, N) and out.dtype in (torch.bfloat16, torch.float32) and out.device == A.codes.device
+    dt = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
+    _check(lib().qfp4_gemm_grouped(ctypes.byref(A.desc), ctypes.byref(B.desc), _ptr(offsets), E, T, _ptr(out),
+                                   _ld(out), dt, _stream(stream)), "qfp4_gemm_grouped")
+    return out
+
+
+def gemm_grouped_wgrad(A: QTensor, B: QTensor, offsets: torch.Tensor, T: int, out_dtype=torch.float32,
+                       out: torch.Tensor | None = None, accumulate: bool = False, stream=None) -> torch.Tensor:
+    """Per group, the product over its tokens [E, A.rows, B.rows]; see qfp4_gemm_grouped_wgrad."""
+    E = _groups(offsets, A.codes)
+    if accumulate and out is None:
+        raise ValueError("accumulate adds into out: pass the buffer")
+    if out is None:
+        out = torch.empty((E, A.rows, B.rows), dtype=out_dtype, device=A.codes.device)
+    assert out.shape == (E, A.rows, B.rows) and out.is_contiguous() and out.device == A.codes.device
+    assert out.dtype in (torch.bfloat16, torch.float32)
+    dt = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
+    _check(lib().qfp4_gemm_grouped_wgrad(ctypes.byref(A.desc), ctypes.byref(B.desc), _ptr(offsets), E, T, _ptr(out), dt,
+                                         1 if accumulate else 0, _stream(stream)), "qfp4_gemm_grouped_wgrad")
+    return out
+
+
+def linear_grouped_workspace_bytes(backward: bool, T: int, E: int, N: int, K: int, rec: Recipe) -> int:
+    return lib().qfp4_linear_grouped_workspace_bytes(1 if backward else 0, T, E, N, K, ctypes.byref(rec))
+
+
+def _linear_grouped_args(X, W, offsets):
+    T, K = X.shape
+    E, N = W.shape[:2]
+    assert X.dtype == W.dtype == torch.bfloat16 and W.shape == (E, N, K) and X.device == W.device
+    assert X.is_contiguous() and W.is_contiguous() and _groups(offsets, X) == E
+    return T, E, N, K
+
+
+def linear_grouped_fwd(X, W, offsets, rec: Recipe, seed: Seed, x_amax=None, Y=None, workspace=None,
+                       stream=None) -> torch.Tensor:
+    """Y[t] = X[t] W_e^T for the rows t of group e, W [E, N, K]; see
+    qfp4_linear_grouped_fwd. Rows of Y that are no group's are not written."""
+    T, E, N, K = _linear_grouped_args(X, W, offsets)
+    Y = torch.empty((T, N), dtype=_dtype(rec.y_dtype), device=X.device) if Y is None else Y
+    assert Y.shape == (T, N) and Y.dtype == _dtype(rec.y_dtype) and Y.is_contiguous() and Y.device == X.device
+    if workspace is None:
+        workspace = torch.empty((linear_grouped_workspace_bytes(False, T, E, N, K, rec),), dtype=torch.uint8,
+                                device=X.device)
+    _check(lib().qfp4_linear_grouped_fwd(_ptr(X), _ptr(W), _ptr(Y), _ptr(offsets), E, T, N, K, ctypes.byref(rec),
+                                         ctypes.byref(seed), _ptr(x_amax), _ptr(workspace), workspace.numel(),
+                                         _stream(stream)), "qfp4_linear_grouped_fwd")
+    return Y
+
+
+def linear_grouped_bwd(dY, X, W, offsets, rec: Recipe, seed: Seed, dX=None, dW=None, workspace=None, stream=None):
+    """(dX, dW) of linear_grouped_fwd; see qfp4_linear_grouped_bwd. Rows of dX
+    that are no group's are not written; dW of an empty group is zero."""
+    T, E, N, K = _linear_grouped_args(X, W, offsets)
+    assert dY.shape == (T, N) and dY.dtype == torch.bfloat16 and dY.is_contiguous() and dY.device == X.device
+    dX = torch.empty((T, K), dtype=_dtype(rec.dx_dtype), device=X.device) if dX is None else dX
+    assert dX.shape == (T, K) and dX.dtype == _dtype(rec.dx_dtype) and dX.is_contiguous() and dX.device == X.device
+    if rec.dw_accumulate and dW is None:
+        raise ValueError("a recipe with dw_accumulate adds into dW: pass the buffer")
+    dW = torch.empty((E, N, K), dtype=_dtype(rec.dw_dtype), device=X.device) if dW is None else dW
+    assert dW.shape == (E, N, K) and dW.dtype == _dtype(rec.dw_dtype) and dW.is_contiguous() and dW.device == X.device
+    if workspace is None:
+        workspace = torch.empty((linear_grouped_workspace_bytes(True, T, E, N, K, rec),), dtype=torch.uint8,
+                                device=X.device)
+    _check(lib().qfp4_linear_grouped_bwd(_ptr(dY), _ptr(X), _ptr(W), _ptr(dX), _ptr(dW), _ptr(offsets), E, T, N, K,
+                                         ctypes.byref(rec), ctypes.byref(seed), _ptr(workspace), workspace.numel(),
+                                         _stream(stream)), "qfp4_linear_grouped_bwd")
+    return dX, dW
+
+
 def status(stream=None):
     """Synchronize and raise if a kernel reported a device-side error."""
     _check(lib().qfp4_status(_stream(stream)), "qfp4_status")
@@ -403,3 +631,44 @@ class Fp4Linear(torch.autograd.Function):
         X, W = ctx.saved_tensors
         dX, dW = linear_bwd(dY.contiguous().to(torch.bfloat16), X.contiguous(), W.contiguous(), ctx.rec, ctx.seed)
         return dX.to(X.dtype), dW.to(W.dtype), None, None
+
+
+class RmsNorm(torch.autograd.Function):
+    """(y, h) = (h / rms(h) * w, x + res) in bf16; res may be None."""
+
+    @staticmethod
+    def forward(ctx, x, res, w, eps: float):
+        C = x.shape[-1]
+        r2 = None if res is None else res.reshape(-1, C)
+        x2 = x.reshape(-1, C)
+        y, h, rstd, _ = rmsnorm_fwd(x2, w, eps, res=r2, h=None if res is not None else torch.empty_like(x2))
+        ctx.save_for_backward(h, w, rstd)
+        ctx.has_res = res is not None
+        return y.view(x.shape), h.view(x.shape)
+
+    @staticmethod
+    def backward(ctx, dy, dh):
+        h, w, rstd = ctx.saved_tensors
+        dx, dw = rmsnorm_bwd(dy.reshape(h.shape).contiguous(), h, w, rstd, dh=dh.reshape(h.shape).contiguous())
+        dx = dx.view(dy.shape)
+        return dx, dx if ctx.has_res else None, dw.to(w.dtype), None
+
+
+class Fp4GroupedLinear(torch.autograd.Function):
+    """y[t] = x[t] W_e^T over the rows t of group e, W [E, N, K] (bf16 inputs,
+    recipe + seed per call). Rows that are no group's give zeros."""
+
+    @staticmethod
+    def forward(ctx, X, W, offsets, rec: Recipe, seed: Seed):
+        ctx.save_for_backward(X, W, offsets)
+        ctx.rec, ctx.seed = rec, seed
+        Y = torch.zeros((X.shape[0], W.shape[1]), dtype=_dtype(rec.y_dtype), device=X.device)
+        return linear_grouped_fwd(X.contiguous(), W.contiguous(), offsets, rec, seed, Y=Y)
+
+    @staticmethod
+    def backward(ctx, dY):
+        X, W, offsets = ctx.saved_tensors
+        dX = torch.zeros(X.shape, dtype=_dtype(ctx.rec.dx_dtype), device=X.device)
+        dX, dW = linear_grouped_bwd(dY.contiguous().to(torch.bfloat16), X.contiguous(), W.contiguous(), offsets,
+                                    ctx.rec, ctx.seed, dX=dX)
+        return dX.to(X.dtype), dW.to(W.dtype), None, None, None

@@ -64,6 +64,9 @@ extern "C" {
 #define QFP4_ERR_BOUNDS (-8)           /* bounds-checked build only: a kernel store fell outside its buffer and was
                                           dropped (from qfp4_status) */
 
+#define QFP4_ERR_OFFSETS (-9)          /* group offsets fall or leave [0, T] (from qfp4_status); the call that read them
+                                          treated every group as empty */
+
 /* ---- enums ---------------------------------------------------------------- */
 /* QFP4_MXFP4_RU: MXFP4 whose shared exponent is rounded up instead of down,
  * E = the smallest exponent with amax_b <= 6 * 2^E, so that no element of a
@@ -370,13 +373,120 @@ int qfp4_linear_fwd_chain(const void* X, const void* W, void* Y, int64_t M, int6
 int qfp4_linear_fwd_noalloc(const void* X, const void* W, void* Y, int64_t M, int64_t N, int64_t K,
                             const qfp4_recipe* recipe, const qfp4_seed* seed, void* stream);
 
+/* ---- RMSNorm ------------------------------------------------------------------
+ * The norm before an FP4 layer, with the residual's addition. x, res, h, y,
+ * dy, dh, dx: bf16, R x C, row strides ld* (elements); w: bf16 [C]; rstd: fp32
+ * [R]. Per row
+ *   h = bf16(x + res)             (res NULL: h = x)
+ *   rstd = fp32(1 / sqrt(sum_j h_j^2 / C + eps)), sum and root in fp64
+ *   y = bf16(fp32(fp32(h * rstd) * w)).
+ * bf16 squares are exact in fp64, so the order of the sum shows in none of the
+ * results but by an fp64 rounding.
+ * qfp4_rmsnorm_fwd: also *y_amax (device fp32, or NULL), what qfp4_amax(y, had,
+ *   ROW, seed) gives, without its read of y: passed to qfp4_linear_fwd_chain,
+ *   qfp4_linear_grouped_fwd (x_amax) or qfp4_quantize (amax_in) it saves an
+ *   NVFP4 layer the amax pass over its input. workspace (with y_amax):
+ *   qfp4_quantize_workspace_bytes().
+ * qfp4_rmsnorm_quantize: also *out, what qfp4_quantize(y, fmt, RTN, had, ROW,
+ *   seed) gives for fmt MXFP4 or MXFP4_RU, without its read of y; y may be
+ *   NULL (not written). The caller sets out's buffers as for qfp4_quantize.
+ * qfp4_rmsnorm_bwd: from dy, the gradient of y, and dh (or NULL), the gradient
+ *   that reaches h another way (the residual stream),
+ *     dx = bf16(rstd * (g - h rstd c) + dh), g = dy * w, c = rstd sum_j(g_j h_j) / C,
+ *   the gradient of x and of res alike, and dw (fp32 [C]) = sum over the rows
+ *   of dy * h * rstd, added to dw with accumulate = 1. fp32 arithmetic; the
+ *   same bits at every call on one kind of GPU. workspace:
+ *   qfp4_rmsnorm_bwd_workspace_bytes(R, C).
+ * Requirements: C a multiple of 16 (32 with a 32-point Hadamard and for the
+ *   quantization), 16 <= C <= QFP4_RMSNORM_MAX_COLS; 0 <= R < 2^31; eps >= 0
+ *   and finite; strides >= C and multiples of 8; matrices, w and the workspace
+ *   16-byte aligned; h required with res. h may be x or res, y may be x, dx may
+ *   be dy or dh (same pointer and stride); no other overlap.
+ * The pages have no counterpart: the norm is what feeds the layers they train. */
+#define QFP4_RMSNORM_MAX_COLS 16384
+int qfp4_rmsnorm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* w, int64_t R, int64_t C,
+                     float eps, void* h, int64_t ldh, void* y, int64_t ldy, float* rstd, int32_t had,
+                     const qfp4_seed* seed, float* y_amax, void* workspace, size_t workspace_bytes, void* stream);
+int qfp4_rmsnorm_quantize(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* w, int64_t R,
+                          int64_t C, float eps, void* h, int64_t ldh, void* y, int64_t ldy, float* rstd, int32_t fmt,
+                          int32_t had, const qfp4_seed* seed, qfp4_tensor* out, void* stream);
+size_t qfp4_rmsnorm_bwd_workspace_bytes(int64_t R, int64_t C);
+int qfp4_rmsnorm_bwd(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* w, const float* rstd,
+                     const void* dh, int64_t lddh, int64_t R, int64_t C, void* dx, int64_t lddx, float* dw,
+                     int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- groups of rows: the experts of a mixture -------------------------------------
+ * T rows (tokens) sorted by expert: group e holds rows [offsets[e],
+ * offsets[e + 1]), offsets a device int32 [E + 1] that never falls and stays in
+ * [0, T]. Groups have any size, none too; rows before offsets[0] and from
+ * offsets[E] on belong to no group and are neither read into a result nor
+ * written. Sizes are read on the device, so calls can be captured and replayed
+ * with other offsets. Offsets that break the rule count as all groups empty
+ * and are reported by qfp4_status (QFP4_ERR_OFFSETS). 1 <= E <= QFP4_MAX_GROUPS.
+ *
+ * Padded layout: group e starts at row p_e = sum_{i<e} 128 ceil(m_i / 128) (m_i
+ * rows in group i), in qfp4_group_rows(T, E) rows in all; every row that is no
+ * group's is zero. Groups then start at whole scale atoms, and along the
+ * tokens no block or Hadamard group holds two experts' rows.
+ *
+ * qfp4_quantize_grouped: exactly what qfp4_quantize gives for the bf16 matrix
+ *   x' of qfp4_group_rows(T, E) rows that holds x (T x C, row stride ld) in the
+ *   padded layout. Requirements: those of qfp4_quantize for x', C a multiple
+ *   of 8; workspace qfp4_quantize_grouped_workspace_bytes(T, C, E).
+ * qfp4_gemm_grouped: D[offsets[e] + i][n] = gA gB sum_k A(p_e + i, k) B_e(n, k)
+ *   for the rows i of each group: A = x' quantized along ROW, D T x N (row
+ *   stride ldd), bf16 or fp32. B_e is group e's part of B, by B's shape: B is
+ *   [E N x K] with the experts along its rows (Fprop: the stacked weights
+ *   quantized along ROW), or [N x E K] with them along the reduction axis
+ *   (Dgrad: the same weights quantized along COL).
+ *   Requirements: as qfp4_gemm; A.rows = qfp4_group_rows(T, E); N a multiple
+ *   of 8; with E > 1, N (first form) or K (second form) a multiple of 128.
+ * qfp4_gemm_grouped_wgrad: D[e][m][n] = gA gB sum_t A(m, t) B(n, t) over group
+ *   e's tokens: A and B quantized along COL, M and N rows; D [E][M][N]
+ *   contiguous, bf16 or fp32, zero for an empty group; accumulate = 1 (fp32):
+ *   D += the product, one fp32 add per element. M a multiple of 128, N of 8.
+ * The products are those of qfp4_gemm group by group; the kernel is its
+ * CTA-pair kernel with a walk over the groups' tiles. Philox streams are
+ * indexed in the padded orientation.
+ *
+ * qfp4_linear_grouped_fwd / _bwd: qfp4_linear_fwd and qfp4_linear_bwd for the
+ *   stacked weights W [E][N][K]: Y[t] = X[t] W_e^T, dX[t] = dY[t] W_e, dW_e =
+ *   dY_e^T X_e (dW [E][N][K]). X [T x K], Y and dY [T x N], contiguous, any T;
+ *   N and K multiples of 128; recipe, seed rule and output types as there
+ *   (dw_accumulate too). An NVFP4 tensor scale covers all groups. x_amax
+ *   (device fp32, or NULL): X's tensor amax for the Fprop rotation, e.g. of
+ *   qfp4_rmsnorm_fwd (ignored unless the Fprop format is NVFP4).
+ * The pages have no mixture of experts; the products are the linear layer's
+ * (page "New AMD paper overturns conventional wisdom: FP4 training...",
+ * section "Poiskovaya eksperimental'naya rabota"). */
+#define QFP4_MAX_GROUPS 256
+int64_t qfp4_group_rows(int64_t T, int32_t E); /* -1 for a bad E or T */
+size_t qfp4_quantize_grouped_workspace_bytes(int64_t T, int64_t C, int32_t E);
+int qfp4_quantize_grouped(const void* x, int64_t T, int64_t C, int64_t ld, const int32_t* offsets, int32_t E,
+                          int32_t fmt, int32_t rounding, int32_t had, int32_t axis, const qfp4_seed* seed,
+                          const float* amax_in, qfp4_tensor* out, void* workspace, size_t workspace_bytes,
+                          void* stream);
+int qfp4_gemm_grouped(const qfp4_tensor* A, const qfp4_tensor* B, const int32_t* offsets, int32_t E, int64_t T, void* D,
+                      int64_t ldd, int32_t out_dtype, void* stream);
+int qfp4_gemm_grouped_wgrad(const qfp4_tensor* A, const qfp4_tensor* B, const int32_t* offsets, int32_t E, int64_t T,
+                            void* D, int32_t out_dtype, int32_t accumulate, void* stream);
+size_t qfp4_linear_grouped_workspace_bytes(int32_t backward, int64_t T, int32_t E, int64_t N, int64_t K,
+                                           const qfp4_recipe* recipe);
+int qfp4_linear_grouped_fwd(const void* X, const void* W, void* Y, const int32_t* offsets, int32_t E, int64_t T,
+                            int64_t N, int64_t K, const qfp4_recipe* recipe, const qfp4_seed* seed,
+                            const float* x_amax, void* workspace, size_t workspace_bytes, void* stream);
+int qfp4_linear_grouped_bwd(const void* dY, const void* X, const void* W, void* dX, void* dW, const int32_t* offsets,
+                            int32_t E, int64_t T, int64_t N, int64_t K, const qfp4_recipe* recipe,
+                            const qfp4_seed* seed, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- status ---------------------------------------------------------------
  * Synchronizes `stream`, then reads and clears the library's device error word
  * on the current device. Returns QFP4_OK, QFP4_ERR_TIMEOUT (a bounded wait in
  * a kernel expired; that kernel skipped the rest of its work), QFP4_ERR_BOUNDS
  * (only from the bounds-checked build, libqfp4_bc.so, compiled with
  * QFP4_BOUNDS_CHECK: a kernel computed a store address outside the output
- * buffer the arguments describe; the store went to a scratch sink instead), or
+ * buffer the arguments describe; the store went to a scratch sink instead),
+ * QFP4_ERR_OFFSETS (a call on groups of rows got bad offsets), or
  * QFP4_ERR_CUDA. */
 int qfp4_status(void* stream);
 
