@@ -20,66 +20,12 @@
 // spans two groups. Rows of D past a group belong to the next one: 32-row
 // boxes that are full leave by TMA, the one a group's end cuts is written row
 // by row from the registers.
+#include "groups.cuh"
 #include "qfp4_device.cuh"
 #include "qfp4_internal.h"
 
 namespace qfp4 {
 namespace {
-
-// The groups as a CTA sees them: row[e] the first row of D, padded[e] the first
-// padded row, tiles[e] the number of 256-row tiles before group e.
-struct GroupTable {
-    int row[kMaxGroups + 1];
-    int padded[kMaxGroups + 1];
-    int tiles[kMaxGroups + 1];
-    __device__ __forceinline__ int size(int e) const { return row[e + 1] - row[e]; }
-};
-
-// Built by one warp. Offsets that fall anywhere or leave [0, T] would lead out
-// of the buffers: they raise the device error word and make every group empty.
-__device__ __forceinline__ void build_groups(GroupTable& g, const int* offsets, int E, int T, int lane) {
-    bool bad = false;
-    for (int e = lane; e <= E; e += 32) {
-        const int o = offsets[e];
-        bad = bad || o < 0 || o > T || (e < E && offsets[e + 1] < o);
-    }
-    bad = __any_sync(0xffffffffu, bad);
-    if (bad && lane == 0 && blockIdx.x == 0) raise_device_error(DEV_ERR_OFFSETS);
-    int padded = 0, tiles = 0;  // of the groups before this step's 32
-    for (int e0 = 0; e0 <= E; e0 += 32) {
-        const int e = e0 + lane;
-        const int o = e <= E && !bad ? offsets[e] : 0;
-        const int m = e < E && !bad ? offsets[e + 1] - o : 0;
-        const int own_a = (m + 127) / 128, own_b = (m + 255) / 256;
-        int a = own_a, b = own_b;
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-            const int ua = __shfl_up_sync(0xffffffffu, a, s), ub = __shfl_up_sync(0xffffffffu, b, s);
-            if (lane >= s) {
-                a += ua;
-                b += ub;
-            }
-        }
-        if (e <= E) {
-            g.row[e] = o;
-            g.padded[e] = (padded + a - own_a) * 128;
-            g.tiles[e] = tiles + b - own_b;
-        }
-        padded += __shfl_sync(0xffffffffu, a, 31);
-        tiles += __shfl_sync(0xffffffffu, b, 31);
-    }
-}
-
-// The group of padded row r, or -1 past the last.
-__device__ __forceinline__ int group_of(const int* first, int E, int r) {
-    if (r >= first[E]) return -1;
-    int lo = 0, hi = E;  // first[lo] <= r < first[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first[mid] <= r) lo = mid; else hi = mid;
-    }
-    return lo;
-}
 
 // One tile of the walk.
 struct GroupTile {
@@ -257,7 +203,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     if (warp == 0) tmem_alloc_pair(tmem_slot, TMEM_COLS);
     pdl_wait();  // the offsets and the operands are written (and the previous readers of D done)
     pdl_launch_dependents();
-    if (warp == 1) build_groups(groups, p.offsets, p.E, p.T, lane);
+    if (warp == 1) build_groups(groups, p.offsets, p.E, p.T, 2 * BM, lane);
     tc_fence_before();
     __syncwarp();
     cluster_sync();  // barriers of both CTAs initialised, tensor memory allocated, groups known
@@ -386,31 +332,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
 }
 
-// xp = the groups' rows of x in the padded layout, zeros in every other row.
-// A warp copies whole rows, 16 bytes per lane and step.
-__global__ void __launch_bounds__(256) group_pad_kernel(const uint4* x, int64_t ld16, int64_t c16, const int* offsets,
-                                                        int E, int T, int Tp, uint4* xp) {
-    __shared__ GroupTable g;
-    pdl_wait();
-    pdl_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp == 0) build_groups(g, offsets, E, T, lane);
-    __syncthreads();
-    const int64_t extent = (int64_t)Tp * c16 * 16;
-    for (int r = blockIdx.x * 8 + warp; r < Tp; r += gridDim.x * 8) {
-        const int e = group_of(g.padded, E, r);
-        const int i = e < 0 ? 0 : r - g.padded[e];
-        const bool have = e >= 0 && i < g.size(e);
-        const uint4* src = x + (have ? (int64_t)(g.row[e] + i) * ld16 : 0);
-        uint4* dst = xp + (int64_t)r * c16;
-#pragma unroll 4
-        for (int64_t c = lane; c < c16; c += 32) {
-            const uint4 v = have ? src[c] : make_uint4(0, 0, 0, 0);
-            *chk(dst + c, xp, extent) = v;
-        }
-    }
-}
-
 }  // namespace
 
 cudaError_t launch_gemm_grouped(const GroupedParams& p, int fmt, bool wgrad, const CUtensorMap* tmapA,
@@ -431,15 +352,6 @@ cudaError_t launch_gemm_grouped(const GroupedParams& p, int fmt, bool wgrad, con
         e = wgrad ? run(gemm_grouped_kernel<kNvfp4, true>) : run(gemm_grouped_kernel<kNvfp4, false>);
     else
         e = wgrad ? run(gemm_grouped_kernel<kMxfp4, true>) : run(gemm_grouped_kernel<kMxfp4, false>);
-    count_launch();
-    return e;
-}
-
-cudaError_t launch_group_pad(const void* x, int64_t ld, int64_t C, const int* offsets, int E, int T, int Tp, void* xp,
-                             int sms, cudaStream_t s) {
-    const int grid = (int)std::min<int64_t>((Tp + 7) / 8, (int64_t)sms * 8);
-    const cudaError_t e = launch_pdl(group_pad_kernel, dim3(grid), dim3(256), 0, s, static_cast<const uint4*>(x), ld / 8,
-                                     C / 8, offsets, E, T, Tp, static_cast<uint4*>(xp));
     count_launch();
     return e;
 }

@@ -192,6 +192,36 @@ int make_row_tmap(CUtensorMap* tm, const void* x, int64_t R, int64_t C, int64_t 
     return QFP4_OK;
 }
 
+// 2-D view of a bf16 R x C tensor for gathered rows: box 64 columns x 1 row
+// (128 bytes), 128-byte swizzle.
+int make_gather_tmap(CUtensorMap* tm, const void* x, int64_t R, int64_t C, int64_t ld) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return cuda_fail(cudaErrorNotSupported);
+    const cuuint64_t dims[2] = {(cuuint64_t)C, (cuuint64_t)R};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, 1};
+    const cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(x), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
+    return QFP4_OK;
+}
+
+// Rows in groups: x has T rows; the R (or k) rows that a quantizer counts are
+// those of the padded layout (see include/qfp4.h).
+struct Groups {
+    const int32_t* offsets;
+    int32_t E;
+    int64_t T;
+};
+void set_groups(QuantParams& p, const Groups* gr) {
+    if (gr == nullptr) return;
+    p.group_offsets = gr->offsets;
+    p.groups = gr->E;
+    p.group_T = (int)gr->T;
+}
+
 // TMA view of x for a pass in the given orientation (G: column-mode group).
 int make_input_tmap(CUtensorMap* tm, const void* x, int64_t R, int64_t C, int64_t ld, int axis, int G) {
     return axis == QFP4_AXIS_ROW ? make_row_tmap(tm, x, R, C, ld) : make_col_tmap(tm, x, R, C, ld, G);
@@ -331,8 +361,10 @@ int validate_input(const void* x, int64_t R, int64_t C, int64_t ld, int32_t had,
 
 // Amax pass into `partials` (their count returned in *n_partials).
 int run_amax(const void* x, int64_t R, int64_t C, int64_t ld, int32_t had, int32_t axis, uint32_t signs,
-             const Geometry& g, float* partials, int* n_partials, int sms, cudaStream_t s) {
+             const Geometry& g, float* partials, int* n_partials, int sms, cudaStream_t s,
+             const Groups* gr = nullptr) {
     QuantParams p{};
+    set_groups(p, gr);
     p.x = static_cast<const uint16_t*>(x);
     p.R = R; p.C = C; p.ld = ld;
     p.rows = g.rows; p.k = g.k;
@@ -341,16 +373,41 @@ int run_amax(const void* x, int64_t R, int64_t C, int64_t ld, int32_t had, int32
     const int nh = had_n(had);
     const int G = col_group(16, nh);
     CUtensorMap tm;
-    int rc = make_input_tmap(&tm, x, R, C, ld, axis, G);
+    int rc = gr ? make_gather_tmap(&tm, x, gr->T, C, ld) : make_input_tmap(&tm, x, R, C, ld, axis, G);
     if (rc) return rc;
     *n_partials = amax_partial_count(sms, quant_tiles(axis, g.rows, g.k, G));
     cudaError_t e = launch_amax(p, axis, nh, &tm, *n_partials, s);
     return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
 }
 
+// qfp4_amax.
+int amax_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t had, int32_t axis, const qfp4_seed* seed,
+              float* amax, void* workspace, size_t workspace_bytes, cudaStream_t s, const Groups* gr = nullptr) {
+    int sms = 0;
+    int rc = bind_context(s);
+    if (rc) return rc;
+    rc = check_device(&sms);
+    if (rc) return rc;
+    Geometry g;
+    if ((rc = validate_input(x, R, C, ld, had, axis, &g))) return rc;
+    if (amax == nullptr || (had_random(had) && seed == nullptr)) return QFP4_ERR_INVALID_ARG;
+    if (workspace == nullptr || workspace_bytes < qfp4_quantize_workspace_bytes()) return QFP4_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return QFP4_ERR_MISALIGNED;
+    if (g.rows == 0 || g.k == 0) {
+        cudaError_t e = cudaMemsetAsync(amax, 0, sizeof(float), s);
+        return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
+    }
+    const uint32_t signs = had_random(had) ? host_sign_bits(seed->rot, seed->rot_stream) : 0u;
+    int n = 0;
+    float* partials = static_cast<float*>(workspace);
+    if ((rc = run_amax(x, R, C, ld, had, axis, signs, g, partials, &n, sms, s, gr))) return rc;
+    cudaError_t e = launch_reduce_max(partials, n, amax, s);
+    return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
+}
+
 int quantize_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t fmt, int32_t rounding, int32_t had,
                   int32_t axis, const qfp4_seed* seed, const float* amax_in, qfp4_tensor* out, void* workspace,
-                  size_t workspace_bytes, cudaStream_t s) {
+                  size_t workspace_bytes, cudaStream_t s, const Groups* gr = nullptr) {
     int sms = 0;
     int rc = bind_context(s);
     if (rc) return rc;
@@ -390,6 +447,7 @@ int quantize_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t fmt, 
     const uint32_t signs = had_random(had) ? host_sign_bits(seed->rot, seed->rot_stream) : 0u;
     const int nh = had_n(had);
     QuantParams p{};
+    set_groups(p, gr);
     p.x = static_cast<const uint16_t*>(x);
     p.R = R; p.C = C; p.ld = ld;
     p.rows = g.rows; p.k = g.k;
@@ -404,12 +462,12 @@ int quantize_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t fmt, 
     p.amax_in = amax_in;
     p.mx_round_up = (fmt == QFP4_MXFP4_RU) ? 1u : 0u;
     // the column quantizer walks 64-row bands when the quantized axis allows it
-    const bool bands = axis == QFP4_AXIS_COL && g.k % 64 == 0 && col_bands_enabled();
+    const bool bands = axis == QFP4_AXIS_COL && g.k % 64 == 0 && (gr != nullptr || col_bands_enabled());
     // An NVFP4 tensor that fits in L2, in the packed unit's cases, is quantized
     // by one cooperative launch that takes its own amax first (the second pass
     // reads from L2) instead of an amax pass, a reduction and the quantizer.
     const bool fused = need_ws && (rounding == QFP4_RTN || rounding == QFP4_QUARTET2) && (nh == 0 || nh == 16) &&
-                       (axis == QFP4_AXIS_ROW || bands) && R * C * 2 <= kFusedAmaxMaxBytes && fused_amax_enabled();
+                       (axis == QFP4_AXIS_ROW || bands) && R * C * 2 <= kFusedAmaxMaxBytes && gr == nullptr && fused_amax_enabled();
     if (fused) {
         float* partials = static_cast<float*>(workspace);
         uint32_t* counter = static_cast<uint32_t*>(workspace) + (kMaxAmaxPartials - 1);
@@ -421,12 +479,14 @@ int quantize_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t fmt, 
     } else if (need_ws) {
         int n = 0;
         float* partials = static_cast<float*>(workspace);
-        if ((rc = run_amax(x, R, C, ld, had, axis, signs, g, partials, &n, sms, s))) return rc;
+        if ((rc = run_amax(x, R, C, ld, had, axis, signs, g, partials, &n, sms, s, gr))) return rc;
         p.amax_partials = partials;
         p.n_partials = n;
     }
     CUtensorMap tm;
-    if (bands)
+    if (gr != nullptr)
+        rc = make_gather_tmap(&tm, x, gr->T, C, ld);
+    else if (bands)
         rc = make_col64_tmap(&tm, x, R, C, ld);
     else
         rc = make_input_tmap(&tm, x, R, C, ld, axis, col_group(NB, nh));
@@ -455,7 +515,8 @@ void fill_out(qfp4_tensor* out, int64_t rows, int64_t k, int32_t fmt, int32_t ha
 
 int quantize_dual_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t fmt, int32_t rounding, int32_t had_row,
                        int32_t had_col, const qfp4_seed* seed_row, const qfp4_seed* seed_col, const float* amax_row,
-                       const float* amax_col, qfp4_tensor* out_row, qfp4_tensor* out_col, cudaStream_t s) {
+                       const float* amax_col, qfp4_tensor* out_row, qfp4_tensor* out_col, cudaStream_t s,
+                       const Groups* gr = nullptr) {
     int sms = 0;
     int rc = bind_context(s);
     if (rc) return rc;
@@ -466,9 +527,9 @@ int quantize_dual_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t 
     if (!out_row || !out_col || !seed_row || !seed_col) return QFP4_ERR_INVALID_ARG;
     for (const qfp4_seed* sd : {seed_row, seed_col})
         if (sd->rot_stream >= (1u << 28) || sd->sr_stream >= (1u << 28)) return QFP4_ERR_INVALID_ARG;
-    Geometry gr, gc;
-    if ((rc = validate_input(x, R, C, ld, had_row, QFP4_AXIS_ROW, &gr))) return rc;
-    if ((rc = validate_input(x, R, C, ld, had_col, QFP4_AXIS_COL, &gc))) return rc;
+    Geometry g_row, g_col;
+    if ((rc = validate_input(x, R, C, ld, had_row, QFP4_AXIS_ROW, &g_row))) return rc;
+    if ((rc = validate_input(x, R, C, ld, had_col, QFP4_AXIS_COL, &g_col))) return rc;
     const int NB = block_of(fmt);
     if (C % NB != 0 || R % NB != 0) return QFP4_ERR_INVALID_ARG;
     if (R == 0 || C == 0) return QFP4_ERR_INVALID_ARG;
@@ -481,6 +542,7 @@ int quantize_dual_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t 
     fill_out(out_row, R, C, fmt, had_row, seed_row);
     fill_out(out_col, C, R, fmt, had_col, seed_col);
     QuantParams p{};
+    set_groups(p, gr);
     p.x = static_cast<const uint16_t*>(x);
     p.R = R; p.C = C; p.ld = ld;
     p.rows = C; p.k = R;  // the column orientation
@@ -504,7 +566,7 @@ int quantize_dual_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t 
     p.sr_tag_elem_row = (uint32_t)kTagElement | (seed_row->sr_stream << 4);
     p.sr_tag_scale_row = (uint32_t)kTagScale | (seed_row->sr_stream << 4);
     CUtensorMap tm;
-    if ((rc = make_col64_tmap(&tm, x, R, C, ld))) return rc;
+    if ((rc = gr ? make_gather_tmap(&tm, x, gr->T, C, ld) : make_col64_tmap(&tm, x, R, C, ld))) return rc;
     const int sfmt = (fmt == QFP4_MXFP4_RU) ? QFP4_MXFP4 : fmt;
     cudaError_t e = launch_quant_dual(p, sfmt, rounding, had_n(had_col), had_n(had_row), &tm, s);
     return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
@@ -721,14 +783,14 @@ qfp4_seed op_seed(const qfp4_seed* s, uint32_t gemm, uint32_t operand) {
 // kernel (its tile serves 16-element groups of both axes); n_h = 32: two passes.
 int amax_rowcol_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t had_row, int32_t had_col,
                      const qfp4_seed* seed_row, const qfp4_seed* seed_col, float* amax_row, float* amax_col,
-                     void* workspace, size_t workspace_bytes, cudaStream_t s) {
+                     void* workspace, size_t workspace_bytes, cudaStream_t s, const Groups* gr = nullptr) {
     int rc = bind_context(s);  // callers may run on threads without a current context
     if (rc) return rc;
     int sms = 0;
     if ((rc = check_device(&sms))) return rc;
-    Geometry gr, gc;
-    if ((rc = validate_input(x, R, C, ld, had_row, QFP4_AXIS_ROW, &gr))) return rc;
-    if ((rc = validate_input(x, R, C, ld, had_col, QFP4_AXIS_COL, &gc))) return rc;
+    Geometry g_row, g_col;
+    if ((rc = validate_input(x, R, C, ld, had_row, QFP4_AXIS_ROW, &g_row))) return rc;
+    if ((rc = validate_input(x, R, C, ld, had_col, QFP4_AXIS_COL, &g_col))) return rc;
     if (amax_row == nullptr || amax_col == nullptr) return QFP4_ERR_INVALID_ARG;
     if ((had_random(had_row) && seed_row == nullptr) || (had_random(had_col) && seed_col == nullptr))
         return QFP4_ERR_INVALID_ARG;
@@ -747,22 +809,23 @@ int amax_rowcol_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t ha
     cudaError_t e;
     if (nh <= 16 && had_n(had_row) == nh) {
         QuantParams p{};
+        set_groups(p, gr);
         p.x = static_cast<const uint16_t*>(x);
         p.R = R; p.C = C; p.ld = ld;
-        p.rows = gc.rows; p.k = gc.k;
+        p.rows = g_col.rows; p.k = g_col.k;
         p.signs = signs_col;
         p.signs_row = signs_row;
         // over 64-row bands when R allows it (both orientations packed), else
         // the group-walking column kernel
-        const bool bands = R % 64 == 0 && col_bands_enabled();
+        const bool bands = R % 64 == 0 && (gr != nullptr || col_bands_enabled());
         const int n = amax_partial_count(
-            sms, bands ? amax_rowcol64_tiles(gc.rows, gc.k) : quant_tiles(QFP4_AXIS_COL, gc.rows, gc.k, 16));
+            sms, bands ? amax_rowcol64_tiles(g_col.rows, g_col.k) : quant_tiles(QFP4_AXIS_COL, g_col.rows, g_col.k, 16));
         if (2 * n > kMaxAmaxPartials) return QFP4_ERR_WORKSPACE;
         p.amax_out = partials;
         p.amax_out_row = partials + n;
         CUtensorMap tm;
         if (bands) {
-            if ((rc = make_col64_tmap(&tm, x, R, C, ld))) return rc;
+            if ((rc = gr ? make_gather_tmap(&tm, x, gr->T, C, ld) : make_col64_tmap(&tm, x, R, C, ld))) return rc;
             e = launch_amax_rowcol64(p, nh, &tm, n, s);
         } else {
             if ((rc = make_input_tmap(&tm, x, R, C, ld, QFP4_AXIS_COL, 16))) return rc;
@@ -773,10 +836,10 @@ int amax_rowcol_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t ha
     } else {
         // a 32-point Hadamard, or Hadamards of different sizes: one pass per orientation
         int n = 0;
-        if ((rc = run_amax(x, R, C, ld, had_row, QFP4_AXIS_ROW, signs_row, gr, partials, &n, sms, s))) return rc;
+        if ((rc = run_amax(x, R, C, ld, had_row, QFP4_AXIS_ROW, signs_row, g_row, partials, &n, sms, s, gr))) return rc;
         e = launch_reduce_max(partials, n, amax_row, s);
         if (e != cudaSuccess) return cuda_fail(e);
-        if ((rc = run_amax(x, R, C, ld, had_col, QFP4_AXIS_COL, signs_col, gc, partials, &n, sms, s))) return rc;
+        if ((rc = run_amax(x, R, C, ld, had_col, QFP4_AXIS_COL, signs_col, g_col, partials, &n, sms, s, gr))) return rc;
         e = launch_reduce_max(partials, n, amax_col, s);
     }
     return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
@@ -837,27 +900,7 @@ size_t qfp4_quantize_workspace_bytes(void) { return (size_t)kMaxAmaxPartials * s
 int qfp4_amax(const void* x, int64_t R, int64_t C, int64_t ld, int32_t had, int32_t axis, const qfp4_seed* seed,
               float* amax, void* workspace, size_t workspace_bytes, void* stream) {
     const ApiRange range("qfp4_amax");
-    int sms = 0;
-    int rc = bind_context(static_cast<cudaStream_t>(stream));
-    if (rc) return rc;
-    rc = check_device(&sms);
-    if (rc) return rc;
-    Geometry g;
-    if ((rc = validate_input(x, R, C, ld, had, axis, &g))) return rc;
-    if (amax == nullptr || (had_random(had) && seed == nullptr)) return QFP4_ERR_INVALID_ARG;
-    if (workspace == nullptr || workspace_bytes < qfp4_quantize_workspace_bytes()) return QFP4_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return QFP4_ERR_MISALIGNED;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (g.rows == 0 || g.k == 0) {
-        cudaError_t e = cudaMemsetAsync(amax, 0, sizeof(float), s);
-        return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
-    }
-    const uint32_t signs = had_random(had) ? host_sign_bits(seed->rot, seed->rot_stream) : 0u;
-    int n = 0;
-    float* partials = static_cast<float*>(workspace);
-    if ((rc = run_amax(x, R, C, ld, had, axis, signs, g, partials, &n, sms, s))) return rc;
-    cudaError_t e = launch_reduce_max(partials, n, amax, s);
-    return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
+    return amax_impl(x, R, C, ld, had, axis, seed, amax, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 int qfp4_amax_rowcol(const void* x, int64_t R, int64_t C, int64_t ld, int32_t had_row, int32_t had_col,
@@ -998,32 +1041,34 @@ int linear_fwd_impl(const void* X, const void* W, void* Y, int64_t M, int64_t N,
 // dy_amax: two floats; partials: the quantizers' workspace.
 int quantize_dy(const void* dY, int64_t M, int64_t N, const qfp4_recipe* recipe, const qfp4_seed* seed,
                 qfp4_tensor* out_row, qfp4_tensor* out_col, float* dy_amax, float* partials, bool* col_done,
-                const float** am_col, cudaStream_t s) {
+                const float** am_col, cudaStream_t s, const Groups* gr = nullptr) {
     const size_t pws = qfp4_quantize_workspace_bytes();
     const qfp4_gemm_cfg& d = recipe->dgrad;
     const qfp4_gemm_cfg& w = recipe->wgrad;
     const qfp4_seed s0 = op_seed(seed, 1, 2), s2 = op_seed(seed, 2, 4);
     const bool dual = d.fmt == w.fmt && d.rnd_a == QFP4_RTN && w.rnd_a == QFP4_RTN && dual_ok(M, d.had, w.had) &&
-                      col_bands_enabled();
+                      (gr != nullptr || col_bands_enabled());
     const float* am_row = nullptr;
     *am_col = nullptr;
     *col_done = dual;
     int rc;
     if (d.fmt == QFP4_NVFP4 && w.fmt == QFP4_NVFP4 && d.had == w.had && had_n(d.had) <= 16) {
-        if ((rc = amax_rowcol_impl(dY, M, N, N, d.had, d.had, &s0, &s2, dy_amax, dy_amax + 1, partials, pws, s)))
+        if ((rc = amax_rowcol_impl(dY, M, N, N, d.had, d.had, &s0, &s2, dy_amax, dy_amax + 1, partials, pws, s,
+                                   gr)))
             return rc;
         am_row = dy_amax;
         *am_col = dy_amax + 1;
     } else if (dual && d.fmt == QFP4_NVFP4) {
-        if ((rc = qfp4_amax(dY, M, N, N, d.had, QFP4_AXIS_ROW, &s0, dy_amax, partials, pws, s))) return rc;
-        if ((rc = qfp4_amax(dY, M, N, N, w.had, QFP4_AXIS_COL, &s2, dy_amax + 1, partials, pws, s))) return rc;
+        if ((rc = amax_impl(dY, M, N, N, d.had, QFP4_AXIS_ROW, &s0, dy_amax, partials, pws, s, gr))) return rc;
+        if ((rc = amax_impl(dY, M, N, N, w.had, QFP4_AXIS_COL, &s2, dy_amax + 1, partials, pws, s, gr))) return rc;
         am_row = dy_amax;
         *am_col = dy_amax + 1;
     }
     if (dual)
         return quantize_dual_impl(dY, M, N, N, d.fmt, d.rnd_a, d.had, w.had, &s0, &s2, am_row, *am_col, out_row,
-                                  out_col, s);
-    return quantize_impl(dY, M, N, N, d.fmt, d.rnd_a, d.had, QFP4_AXIS_ROW, &s0, am_row, out_row, partials, pws, s);
+                                  out_col, s, gr);
+    return quantize_impl(dY, M, N, N, d.fmt, d.rnd_a, d.had, QFP4_AXIS_ROW, &s0, am_row, out_row, partials, pws, s,
+                         gr);
 }
 }  // namespace
 }  // namespace qfp4
@@ -1249,18 +1294,6 @@ int gemm_grouped_wgrad_impl(const qfp4_tensor* A, const qfp4_tensor* B, const in
     return run_grouped(A, B, true, M * E, p, sms, s);
 }
 
-// xp = x in the padded layout.
-int group_pad(const void* x, int64_t T, int64_t C, int64_t ld, const int32_t* offsets, int32_t E, void* xp,
-              cudaStream_t s) {
-    int sms = 0;
-    int rc = bind_context(s);
-    if (rc) return rc;
-    if ((rc = check_device(&sms))) return rc;
-    if (T == 0 || C == 0) return QFP4_OK;
-    const cudaError_t e = launch_group_pad(x, ld, C, offsets, E, (int)T, (int)group_rows(T, E), xp, sms, s);
-    return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
-}
-
 int quantize_grouped_impl(const void* x, int64_t T, int64_t C, int64_t ld, const int32_t* offsets, int32_t E,
                           int32_t fmt, int32_t rounding, int32_t had, int32_t axis, const qfp4_seed* seed,
                           const float* amax_in, qfp4_tensor* out, void* workspace, size_t workspace_bytes,
@@ -1281,16 +1314,13 @@ int quantize_grouped_impl(const void* x, int64_t T, int64_t C, int64_t ld, const
         if (out->codes == nullptr || out->scales == nullptr) return QFP4_ERR_INVALID_ARG;
         if (!aligned16(out->codes) || !aligned16(out->scales)) return QFP4_ERR_MISALIGNED;
     }
-    if (workspace == nullptr || workspace_bytes < qfp4_quantize_grouped_workspace_bytes(T, C, E))
-        return QFP4_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return QFP4_ERR_MISALIGNED;
-    Carver c{static_cast<uint8_t*>(workspace), 0};
-    void* partials = c.take(qfp4_quantize_workspace_bytes());
-    const int64_t Tp = group_rows(T, E);
-    void* xp = c.take((size_t)(Tp * C) * 2);
-    if ((rc = group_pad(x, T, C, ld, offsets, E, xp, s))) return rc;
-    return quantize_impl(xp, Tp, C, C, fmt, rounding, had, axis, seed, amax_in, out, partials,
-                         qfp4_quantize_workspace_bytes(), s);
+    if (fmt == QFP4_NVFP4 && amax_in == nullptr && T > 0 && C > 0) {
+        if (workspace == nullptr || workspace_bytes < qfp4_quantize_workspace_bytes()) return QFP4_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return QFP4_ERR_MISALIGNED;
+    }
+    const Groups gr{offsets, E, T};
+    return quantize_impl(x, group_rows(T, E), C, ld, fmt, rounding, had, axis, seed, amax_in, out, workspace,
+                         workspace_bytes, s, &gr);
 }
 
 // ---- linear layer of a mixture of experts -----------------------------------------
@@ -1306,8 +1336,6 @@ int check_linear_grouped(const int32_t* offsets, int32_t E, int64_t T, int64_t N
 struct GroupedLayout {
     float* partials;
     float* dy_amax;
-    void* xp;       // X in the padded layout
-    void* dyp;      // dY in the padded layout
     qfp4_tensor t[4];
     size_t total;
 };
@@ -1317,13 +1345,11 @@ GroupedLayout grouped_layout(int backward, int64_t T, int32_t E, int64_t N, int6
     Carver c{ws, 0};
     const int64_t Tp = group_rows(T, E);
     l.partials = static_cast<float*>(c.take(qfp4_quantize_workspace_bytes()));
-    l.xp = c.take((size_t)(Tp * K) * 2);
     if (!backward) {
         carve_operand(c, &l.t[0], r->fprop.fmt, Tp, K);     // X along K
         carve_operand(c, &l.t[1], r->fprop.fmt, N * E, K);  // W along K
     } else {
         l.dy_amax = static_cast<float*>(c.take(2 * sizeof(float)));
-        l.dyp = c.take((size_t)(Tp * N) * 2);
         carve_operand(c, &l.t[0], r->dgrad.fmt, Tp, N);     // dY along N
         carve_operand(c, &l.t[1], r->dgrad.fmt, K, N * E);  // W^T: W along N
         carve_operand(c, &l.t[2], r->wgrad.fmt, N, Tp);     // dY^T: dY along the tokens
@@ -1433,14 +1459,6 @@ int64_t qfp4_group_rows(int64_t T, int32_t E) {
     return E < 1 || E > QFP4_MAX_GROUPS || T < 0 ? -1 : group_rows(T, E);
 }
 
-size_t qfp4_quantize_grouped_workspace_bytes(int64_t T, int64_t C, int32_t E) {
-    if (T < 0 || C < 0 || E < 1 || E > QFP4_MAX_GROUPS) return 0;
-    Carver c{nullptr, 0};
-    c.take(qfp4_quantize_workspace_bytes());
-    c.take((size_t)(group_rows(T, E) * C) * 2);
-    return c.off;
-}
-
 int qfp4_quantize_grouped(const void* x, int64_t T, int64_t C, int64_t ld, const int32_t* offsets, int32_t E,
                           int32_t fmt, int32_t rounding, int32_t had, int32_t axis, const qfp4_seed* seed,
                           const float* amax_in, qfp4_tensor* out, void* workspace, size_t workspace_bytes,
@@ -1489,9 +1507,9 @@ int qfp4_linear_grouped_fwd(const void* X, const void* W, void* Y, const int32_t
     const int64_t Tp = group_rows(T, E);
     const qfp4_seed sx = op_seed(seed, 0, 0), sw = op_seed(seed, 0, 1);
     const float* ax = c.fmt == QFP4_NVFP4 ? x_amax : nullptr;
-    if ((rc = group_pad(X, T, K, K, offsets, E, l.xp, s))) return rc;
-    if ((rc = quantize_impl(l.xp, Tp, K, K, c.fmt, c.rnd_a, c.had, QFP4_AXIS_ROW, &sx, ax, &l.t[0], l.partials, pws,
-                            s)))
+    const Groups gr{offsets, E, T};
+    if ((rc = quantize_impl(X, Tp, K, K, c.fmt, c.rnd_a, c.had, QFP4_AXIS_ROW, &sx, ax, &l.t[0], l.partials, pws, s,
+                            &gr)))
         return rc;
     if ((rc = quantize_impl(W, N * E, K, K, c.fmt, c.rnd_b, c.had, QFP4_AXIS_ROW, &sw, nullptr, &l.t[1], l.partials,
                             pws, s)))
@@ -1527,8 +1545,9 @@ int qfp4_linear_grouped_bwd(const void* dY, const void* X, const void* W, void* 
     const qfp4_seed s1 = op_seed(seed, 1, 3), s2 = op_seed(seed, 2, 4), s3 = op_seed(seed, 2, 5);
     bool dy_done;
     const float* dy_am_col;
-    if ((rc = group_pad(dY, T, N, N, offsets, E, l.dyp, s))) return rc;
-    if ((rc = quantize_dy(l.dyp, Tp, N, recipe, seed, &l.t[0], &l.t[2], l.dy_amax, l.partials, &dy_done, &dy_am_col, s)))
+    const Groups gr{offsets, E, T};
+    if ((rc = quantize_dy(dY, Tp, N, recipe, seed, &l.t[0], &l.t[2], l.dy_amax, l.partials, &dy_done, &dy_am_col, s,
+                          &gr)))
         return rc;
     // Dgrad dX[e] = dY[e] . W[e]: reduce over N, W's experts along the reduction axis.
     if ((rc = quantize_impl(W, N * E, K, K, d.fmt, d.rnd_b, d.had, QFP4_AXIS_COL, &s1, nullptr, &l.t[1], l.partials, pws,
@@ -1536,12 +1555,11 @@ int qfp4_linear_grouped_bwd(const void* dY, const void* X, const void* W, void* 
         return rc;
     if ((rc = gemm_grouped_impl(&l.t[0], &l.t[1], offsets, E, T, dX, K, recipe->dx_dtype, s))) return rc;
     // Wgrad dW[e] = dY[e]^T . X[e]: reduce over the group's tokens.
-    if (!dy_done && (rc = quantize_impl(l.dyp, Tp, N, N, w.fmt, w.rnd_a, w.had, QFP4_AXIS_COL, &s2, dy_am_col, &l.t[2],
-                                        l.partials, pws, s)))
+    if (!dy_done && (rc = quantize_impl(dY, Tp, N, N, w.fmt, w.rnd_a, w.had, QFP4_AXIS_COL, &s2, dy_am_col, &l.t[2],
+                                        l.partials, pws, s, &gr)))
         return rc;
-    if ((rc = group_pad(X, T, K, K, offsets, E, l.xp, s))) return rc;
-    if ((rc = quantize_impl(l.xp, Tp, K, K, w.fmt, w.rnd_b, w.had, QFP4_AXIS_COL, &s3, nullptr, &l.t[3], l.partials, pws,
-                            s)))
+    if ((rc = quantize_impl(X, Tp, K, K, w.fmt, w.rnd_b, w.had, QFP4_AXIS_COL, &s3, nullptr, &l.t[3], l.partials, pws,
+                            s, &gr)))
         return rc;
     return gemm_grouped_wgrad_impl(&l.t[2], &l.t[3], offsets, E, T, dW, recipe->dw_dtype, dw_add, s);
 }

@@ -16,6 +16,9 @@ constexpr int kTagElement = 0, kTagScale = 1, kTagSign = 2;
 // Upper bound on the number of per-CTA amax partials (the workspace holds them).
 constexpr int kMaxAmaxPartials = 1024;
 
+// Most groups of rows a call takes.
+constexpr int kMaxGroups = 256;
+
 struct QuantParams {
     const uint16_t* x;  // bf16 input, R x C, row stride ld
     int64_t R, C, ld;
@@ -52,6 +55,12 @@ struct QuantParams {
     // arrival counter, zeroed before the launch; the partials go to amax_out
     // and are read back through amax_partials.
     uint32_t* grid_counter;
+    // Rows in groups (nullptr: none): x then has group_T rows in `groups`
+    // groups, and R (and so rows or k) counts those of the padded layout. tmap
+    // is the 2-D view whose boxes are one row high; the rows of a tile are
+    // gathered.
+    const int* group_offsets;
+    int groups, group_T;
 };
 
 // Launchers (quant.cu). Return cudaSuccess or the launch error.
@@ -177,7 +186,6 @@ cudaError_t launch_rmsnorm_bwd(const NormBwdParams& p, float* dw, int accumulate
 // grouped_sm100.cu: rows in groups (the experts of a mixture). offsets: device
 // int32 [E + 1], group e's rows are [offsets[e], offsets[e + 1]) of T; in the
 // padded layout it starts at row sum_{i<e} 128 ceil(m_i / 128) of Tp.
-constexpr int kMaxGroups = 256;
 struct GroupedParams {
     const int* offsets;
     int E, T, Tp;
@@ -198,10 +206,6 @@ struct GroupedParams {
 cudaError_t launch_gemm_grouped(const GroupedParams& p, int fmt, bool wgrad, const CUtensorMap* tmapA,
                                 const CUtensorMap* tmapB, const CUtensorMap* tmapSFA, const CUtensorMap* tmapSFB,
                                 const CUtensorMap* tmapD, cudaStream_t s, int sms);
-// xp [Tp x C] (contiguous) = the groups' rows of x in the padded layout, zeros elsewhere.
-cudaError_t launch_group_pad(const void* x, int64_t ld, int64_t C, const int* offsets, int E, int T, int Tp, void* xp,
-                             int sms, cudaStream_t s);
-
 void count_launch();
 
 }  // namespace qfp4

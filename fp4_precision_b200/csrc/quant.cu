@@ -27,6 +27,7 @@
 // stride, written out as __fmaf_rn / __ffma2_rn; the library is built with
 // --fmad=false, and packed f32x2 operations round each lane like the scalar
 // instruction), so codes and scales are exactly those of the definition.
+#include "groups.cuh"
 #include "qfp4_device.cuh"
 #include "qfp4_internal.h"
 
@@ -769,6 +770,82 @@ __device__ __forceinline__ void ring_init(Ring<STAGES>& ring) {
     fence_mbarrier_init();
 }
 
+// ---------------------------------------------------------------------------
+// Rows in groups: the tile's rows are those of the padded layout, gathered from
+// the groups' own rows by TMA (four per instruction, any rows); a row that is
+// no group's is read past the tensor and so zero. Only the producer differs:
+// the compute warps see a tile of the padded matrix. The kernels take this as a
+// template flag: as a branch at run time it cost the kernels without groups 1 %. One instruction per 512
+// bytes instead of one per tile, issued by the whole producer warp.
+
+// x-row (within the tile) that shared-memory row s holds.
+struct RowOrder {
+    __device__ static int row(int s) { return s; }
+};
+struct BandOrder {  // 64-row bands
+    __device__ static int row(int s) { return (s & 1) + 2 * (s >> 3) + 64 * ((s >> 1) & 3); }
+};
+template <int G>
+struct ColOrder {
+    __device__ static int row(int s) { return (s & 1) + 2 * ((s >> 3) & 3) + 8 * (s >> 5) + G * ((s >> 1) & 3); }
+};
+
+// The table and, per ring stage, the rows that groups have in each 128-row
+// half of the tile; behind the ring in dynamic shared memory.
+template <int STAGES>
+struct GroupSmem {
+    GroupTable table;
+    int rows[STAGES][2];
+};
+
+// The producer warp of a kernel whose tiles are ROWS x (64 BOXES).
+template <int STAGES, int ROWS, int BOXES, typename Order>
+__device__ __forceinline__ void gather_tiles(const void* tmap, const int* offsets, int groups, int T, Ring<STAGES>& ring,
+                                          uint8_t* tiles, int tiles_c, int tiles_r, int lane) {
+    GroupSmem<STAGES>& gs = *reinterpret_cast<GroupSmem<STAGES>*>(tiles + STAGES * BOXES * ROWS * 128);
+    constexpr int BOX_BYTES = ROWS * 128;
+    build_groups(gs.table, offsets, groups, T, 128, lane);
+    __syncwarp();
+    int i = 0;
+    for (TileWalk<STAGES> w(tiles_c); w.tr < tiles_r; w.next(), ++i) {
+        const int s = w.stage;
+        const bool ok = i < STAGES || mbar_wait(&ring.empty[s], w.phase ^ 1u);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        int src = 0, n = 0;  // lanes 0 and 1: first source row of the half, its rows
+        if (lane < (ROWS + 127) / 128) {
+            const int r = w.tr * ROWS + lane * 128;
+            const int e = group_of(gs.table.padded, groups, r);
+            if (e >= 0) {
+                const int at = r - gs.table.padded[e];
+                src = gs.table.row[e] + at;
+                n = min(128, max(0, gs.table.size(e) - at));
+            }
+            gs.rows[s][lane] = n;
+        }
+        const int src0 = __shfl_sync(0xffffffffu, src, 0), src1 = __shfl_sync(0xffffffffu, src, 1);
+        const int n0 = __shfl_sync(0xffffffffu, n, 0), n1 = __shfl_sync(0xffffffffu, n, 1);
+        if (lane == 0) mbar_arrive_expect_tx(&ring.full[s], BOXES * BOX_BYTES);
+        __syncwarp();
+#pragma unroll
+        for (int s0 = 0; s0 < ROWS; s0 += 128) {
+            const int s4 = s0 + 4 * lane;
+            if (s4 < ROWS) {
+                int y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = Order::row(s4 + j), at = r & 127;
+                    y[j] = r < 128 ? (at < n0 ? src0 + at : T) : (at < n1 ? src1 + at : T);
+                }
+#pragma unroll
+                for (int b = 0; b < BOXES; ++b)
+                    tma_gather4(tiles + s * (BOXES * BOX_BYTES) + b * BOX_BYTES + s4 * 128, tmap, &ring.full[s],
+                                (w.tc * BOXES + b) * 64, y[0], y[1], y[2], y[3]);
+            }
+        }
+    }
+    if (lane == 0) drain_loads(ring.full, nullptr, STAGES, i);  // no load lands after this CTA exits
+}
+
 // CTA-wide max over the compute warps' values; thread 0 writes the partial.
 __device__ __forceinline__ void write_partial(float m, float* red, float* out) {
 #pragma unroll
@@ -852,7 +929,7 @@ constexpr bool issue_bound_mode() {
 // FUSED: an NVFP4 tensor that fits in L2 in one cooperative launch — a first
 // pass over the tiles takes the rotated amax, a grid barrier, then the
 // quantizing pass re-reads the tiles (from L2).
-template <int FMT, int RND, int NH, bool AMAX_ONLY, int STAGES, bool FUSED = false>
+template <int FMT, int RND, int NH, bool AMAX_ONLY, int STAGES, bool FUSED = false, bool GROUPED = false>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
     quant_row_kernel(const __grid_constant__ CUtensorMap tmap, const QuantParams p) {
     using Grp = Group<FMT, RND, NH>;
@@ -881,6 +958,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
     pdl_launch_dependents();
 
     if (warp == kComputeWarps) {
+        if constexpr (GROUPED) {
+            gather_tiles<STAGES, kRowTileRows, 1, RowOrder>(&tmap, p.group_offsets, p.groups, p.group_T, ring, tiles,
+                                                           tiles_c, tiles_r, lane);
+            return;
+        }
         // ---------------- producer ----------------
         if (lane == 0) {
             int i = 0;
@@ -954,7 +1036,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
         uint32_t codes[kRowTileCols / 8];
         uint32_t scodes[kRowTileCols / 16];
         uint32_t scw = 0;
-        if constexpr (kPacked) {
+        // rows in groups: a warp whose rows are all no group's has zero codes and scales
+        bool nothing = false;
+        if constexpr (GROUPED)
+            nothing = ((warp & 3) << 5) >=
+                      reinterpret_cast<GroupSmem<STAGES>*>(tiles + STAGES * STAGE_BYTES)->rows[s][warp >> 2];
+        if (nothing) {
+#pragma unroll
+            for (int i = 0; i < kRowTileCols / 8; ++i) codes[i] = 0;
+#pragma unroll
+            for (int i = 0; i < kRowTileCols / 16; ++i) scodes[i] = 0;
+        } else if constexpr (kPacked) {
             // chunk c of this thread's row: 16-byte chunk c ^ (tid % 8) of its 128-byte line
             const uint32_t rb = smem_u32(tiles) + (uint32_t)(s * STAGE_BYTES) + (uint32_t)tid * 128u +
                                 ((uint32_t)(tid & 7) << 4);
@@ -1050,7 +1142,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
 // Lane l of an ldmatrix.x4 supplies row l % 8 of matrix l / 8, i.e. smem row
 // s = l + 32u; after the transposing load, lane (c = l / 4, q = l % 4) holds
 // x-rows Gq + 8u + [0, 8) of column c.
-template <int FMT, int RND, int NH, bool AMAX_ONLY, int STAGES, bool DUAL = false>
+template <int FMT, int RND, int NH, bool AMAX_ONLY, int STAGES, bool DUAL = false, bool GROUPED = false>
 __global__ void __launch_bounds__(kThreads, 2)
     quant_col_kernel(const __grid_constant__ CUtensorMap tmap, const QuantParams p) {
     using Grp = Group<FMT, RND, NH>;
@@ -1077,6 +1169,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     pdl_launch_dependents();
 
     if (warp == kComputeWarps) {
+        if constexpr (GROUPED) {
+            gather_tiles<STAGES, TILE_ROWS, 2, ColOrder<G>>(&tmap, p.group_offsets, p.groups, p.group_T, ring, tiles,
+                                                           tiles_c, tiles_r, lane);
+            return;
+        }
         if (lane == 0) {
             int i = 0;
             for (TileWalk<STAGES> w(tiles_c); w.tr < tiles_r; w.next(), ++i) {
@@ -1388,7 +1485,7 @@ __device__ __forceinline__ void dual_row_work(const QuantParams& p, float s_enc_
 // 64 columns, in the row orientation (rotation of size NH_ROW with the row
 // sign vector, the row tensor amax and random streams), as the row kernel
 // would: one read of x gives both orientations.
-template <int FMT, int RND, int NH, int STAGES, int NH_ROW = -1, bool FUSED = false>
+template <int FMT, int RND, int NH, int STAGES, int NH_ROW = -1, bool FUSED = false, bool GROUPED = false>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
     quant_col64_kernel(const __grid_constant__ CUtensorMap tmap, const QuantParams p) {
     constexpr bool kDual = NH_ROW >= 0;
@@ -1423,6 +1520,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
     pdl_launch_dependents();
 
     if (warp == kComputeWarps) {
+        if constexpr (GROUPED) {
+            gather_tiles<STAGES, TILE_ROWS, 1, BandOrder>(&tmap, p.group_offsets, p.groups, p.group_T, ring, tiles,
+                                                           tiles_c, tiles_r, lane);
+            return;
+        }
         if (lane == 0) {
             int i = 0;
             bool ok = true;
@@ -1593,7 +1695,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
 // 1/sqrt(n_h) is applied once to each CTA's maxima (rounding c * y is
 // monotone in y). Zero-filled columns and rows past the tensor add nothing.
 
-template <int NH, int STAGES>
+template <int NH, int STAGES, bool GROUPED = false>
 __global__ void __launch_bounds__(kThreads, 2)
     amax_rowcol64_kernel(const __grid_constant__ CUtensorMap tmap, const QuantParams p) {
     static_assert(NH == 0 || NH == 16, "16-element groups");
@@ -1615,6 +1717,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     pdl_wait();  // the previous kernel's writes are visible (and its reads done)
     pdl_launch_dependents();
     if (warp == kComputeWarps) {
+        if constexpr (GROUPED) {
+            gather_tiles<STAGES, TILE_ROWS, 1, BandOrder>(&tmap, p.group_offsets, p.groups, p.group_T, ring, tiles,
+                                                           tiles_c, tiles_r, lane);
+            return;
+        }
         if (lane == 0) {
             int i = 0;
             for (TileWalk<STAGES> w(tiles_c); w.tr < tiles_r; w.next(), ++i) {
@@ -1666,6 +1773,12 @@ int persistent_grid(int64_t tiles, int per_sm) {
     return g < 1 ? 1 : (int)g;
 }
 
+// Dynamic shared memory of a ring of STAGES stages.
+template <int STAGES>
+int ring_smem(int stage_bytes, const QuantParams& p) {
+    return STAGES * stage_bytes + 1024 + (p.group_offsets != nullptr ? (int)sizeof(GroupSmem<STAGES>) : 0);
+}
+
 template <typename Kern>
 cudaError_t launch_persistent(Kern kern, int grid, int smem, const CUtensorMap& tmap, const QuantParams& p,
                               cudaStream_t s) {
@@ -1711,7 +1824,9 @@ cudaError_t launch_t(const QuantParams& p, int axis, const CUtensorMap* tmap, in
             ((p.rows + kRowTileRows - 1) / kRowTileRows) * ((p.k + kRowTileCols - 1) / kRowTileCols);
         constexpr int S = (!AMAX_ONLY && issue_bound_mode<FMT, RND>()) ? 2 : kRowStages;
         if (grid <= 0) grid = persistent_grid(tiles, kCtasPerSm<S>);
-        const int smem = S * kRowTileRows * kRowTileCols * 2 + 1024;
+        const int smem = ring_smem<S>(kRowTileRows * kRowTileCols * 2, p);
+        if (p.group_offsets != nullptr)
+            return launch_persistent(quant_row_kernel<FMT, RND, NH, AMAX_ONLY, S, false, true>, grid, smem, *tmap, p, s);
         return launch_persistent(quant_row_kernel<FMT, RND, NH, AMAX_ONLY, S>, grid, smem, *tmap, p, s);
     } else {
         constexpr int NB = (FMT == kNvfp4) ? 16 : 32;
@@ -1719,7 +1834,12 @@ cudaError_t launch_t(const QuantParams& p, int axis, const CUtensorMap* tmap, in
         constexpr int S = col_stages<G>();
         const int64_t tiles = ((p.rows + kColTileCols - 1) / kColTileCols) * ((p.k + 4 * G - 1) / (4 * G));
         if (grid <= 0) grid = persistent_grid(tiles, 2);
-        const int smem = S * 2 * (4 * G * 64 * 2) + 1024;
+        const int smem = ring_smem<S>(2 * (4 * G * 64 * 2), p);
+        // rows in groups come here for the amax alone (they are quantized over bands)
+        if constexpr (AMAX_ONLY)
+            if (p.group_offsets != nullptr)
+                return launch_persistent(quant_col_kernel<FMT, RND, NH, AMAX_ONLY, S, false, true>, grid, smem, *tmap, p,
+                                         s);
         return launch_persistent(quant_col_kernel<FMT, RND, NH, AMAX_ONLY, S>, grid, smem, *tmap, p, s);
     }
 }
@@ -1729,7 +1849,10 @@ template <int FMT, int RND, int NH>
 cudaError_t launch_col64(const QuantParams& p, const CUtensorMap* tmap, cudaStream_t s) {
     constexpr int S = issue_bound_mode<FMT, RND>() ? 2 : 3;
     const int64_t tiles = ((p.rows + 127) / 128 * 2) * ((p.k + 255) / 256);
-    const int smem = S * 256 * 64 * 2 + 1024;
+    const int smem = ring_smem<S>(256 * 64 * 2, p);
+    if (p.group_offsets != nullptr)
+        return launch_persistent(quant_col64_kernel<FMT, RND, NH, S, -1, false, true>,
+                                 persistent_grid(tiles, kCtasPerSm<S>), smem, *tmap, p, s);
     return launch_persistent(quant_col64_kernel<FMT, RND, NH, S>, persistent_grid(tiles, kCtasPerSm<S>), smem,
                              *tmap, p, s);
 }
@@ -1823,7 +1946,12 @@ template <int FMT, int RND, int NH, int NH_ROW>
 cudaError_t launch_dual_t(const QuantParams& p, const CUtensorMap* tmap, cudaStream_t s) {
     constexpr int S = 3;
     const int64_t tiles = ((p.rows + 127) / 128 * 2) * ((p.k + 255) / 256);
-    const int smem = S * 256 * 64 * 2 + 1024;
+    const int smem = ring_smem<S>(256 * 64 * 2, p);
+    // rows in groups come here to be rounded to nearest alone (the linear layer's one read of dY)
+    if constexpr (RND == kRtn)
+        if (p.group_offsets != nullptr)
+            return launch_persistent(quant_col64_kernel<FMT, RND, NH, S, NH_ROW, false, true>, persistent_grid(tiles, 2),
+                                     smem, *tmap, p, s);
     return launch_persistent(quant_col64_kernel<FMT, RND, NH, S, NH_ROW>, persistent_grid(tiles, 2), smem, *tmap, p,
                              s);
 }
@@ -1850,7 +1978,10 @@ cudaError_t launch_quant_dual(const QuantParams& p, int fmt, int rnd, int nh, in
 cudaError_t launch_amax_rowcol64(const QuantParams& p, int nh, const CUtensorMap* tmap, int n_partials,
                                  cudaStream_t s) {
     constexpr int S = 3;
-    const int smem = S * 256 * 64 * 2 + 1024;
+    const int smem = ring_smem<S>(256 * 64 * 2, p);
+    if (p.group_offsets != nullptr)
+        return nh == 16 ? launch_persistent(amax_rowcol64_kernel<16, S, true>, n_partials, smem, *tmap, p, s)
+                        : launch_persistent(amax_rowcol64_kernel<0, S, true>, n_partials, smem, *tmap, p, s);
     if (nh == 16) return launch_persistent(amax_rowcol64_kernel<16, S>, n_partials, smem, *tmap, p, s);
     return launch_persistent(amax_rowcol64_kernel<0, S>, n_partials, smem, *tmap, p, s);
 }

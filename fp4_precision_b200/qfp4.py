@@ -109,7 +109,6 @@ _SIGNATURES = {
     "qfp4_rmsnorm_bwd": (ctypes.c_int, [_VOID, _I64, _VOID, _I64, _VOID, _VOID, _VOID, _I64, _I64, _I64, _VOID, _I64,
                                         _VOID, _I32, _VOID, _SZ, _VOID]),
     "qfp4_group_rows": (_I64, [_I64, _I32]),
-    "qfp4_quantize_grouped_workspace_bytes": (_SZ, [_I64, _I64, _I32]),
     "qfp4_quantize_grouped": (ctypes.c_int, [_VOID, _I64, _I64, _I64, _VOID, _I32, _I32, _I32, _I32, _I32,
                                              ctypes.POINTER(Seed), _VOID, ctypes.POINTER(TensorDesc), _VOID, _SZ,
                                              _VOID]),
@@ -512,8 +511,7 @@ def quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, fmt: int, rounding:
     rows, k = (Tp, C) if axis == ROW else (C, Tp)
     out = empty_qtensor(fmt, max(rows, 0), max(k, 0), x.device) if out is None else out
     if workspace is None:
-        workspace = torch.empty((lib().qfp4_quantize_grouped_workspace_bytes(T, C, E),), dtype=torch.uint8,
-                                device=x.device)
+        workspace = torch.empty((quantize_workspace_bytes(),), dtype=torch.uint8, device=x.device)
     seed = seed or make_seed()
     _check(lib().qfp4_quantize_grouped(_ptr(x), T, C, _ld(x), _ptr(offsets), E, fmt, rounding, had, axis,
                                        ctypes.byref(seed), _ptr(amax_in), ctypes.byref(out.desc), _ptr(workspace),

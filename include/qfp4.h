@@ -432,7 +432,7 @@ int qfp4_rmsnorm_bwd(const void* dy, int64_t lddy, const void* h, int64_t ldh, c
  * qfp4_quantize_grouped: exactly what qfp4_quantize gives for the bf16 matrix
  *   x' of qfp4_group_rows(T, E) rows that holds x (T x C, row stride ld) in the
  *   padded layout. Requirements: those of qfp4_quantize for x', C a multiple
- *   of 8; workspace qfp4_quantize_grouped_workspace_bytes(T, C, E).
+ *   of 8; workspace as qfp4_quantize. x is read where it lies.
  * qfp4_gemm_grouped: D[offsets[e] + i][n] = gA gB sum_k A(p_e + i, k) B_e(n, k)
  *   for the rows i of each group: A = x' quantized along ROW, D T x N (row
  *   stride ldd), bf16 or fp32. B_e is group e's part of B, by B's shape: B is
@@ -461,7 +461,6 @@ int qfp4_rmsnorm_bwd(const void* dy, int64_t lddy, const void* h, int64_t ldh, c
  * section "Poiskovaya eksperimental'naya rabota"). */
 #define QFP4_MAX_GROUPS 256
 int64_t qfp4_group_rows(int64_t T, int32_t E); /* -1 for a bad E or T */
-size_t qfp4_quantize_grouped_workspace_bytes(int64_t T, int64_t C, int32_t E);
 int qfp4_quantize_grouped(const void* x, int64_t T, int64_t C, int64_t ld, const int32_t* offsets, int32_t E,
                           int32_t fmt, int32_t rounding, int32_t had, int32_t axis, const qfp4_seed* seed,
                           const float* amax_in, qfp4_tensor* out, void* workspace, size_t workspace_bytes,
