@@ -13,7 +13,7 @@
 //          the reduction axis (Dgrad: W^T as [K x E N]).
 //   wgrad: D[e] = gA gB sum over group e's tokens t of A[.][t] B[.][t]^T.
 //
-// The kernel is the dense CTA-pair kernel (256 x 256 tiles, tcgen05
+// The main kernel is the dense CTA-pair kernel (256 x 256 tiles, tcgen05
 // cta_group::2, the same warp roles and rings) with another walk: every role
 // finds a tile's group by a binary search over prefix sums of the tile counts
 // in shared memory, which the CTA builds once from the offsets. A tile never
@@ -34,14 +34,14 @@ struct GroupTile {
     int k0, k;   // first element of the reduction in A, its length
 };
 
-template <bool WGRAD>
+template <bool WGRAD, int TILE_M>
 struct GroupWalk {
     const GroupTable& g;
     const GroupedParams& p;
     int num_m, num_n, total;
     __device__ __forceinline__ GroupWalk(const GroupTable& t, const GroupedParams& q) : g(t), p(q) {
         num_n = (p.N + kGemmBN - 1) / kGemmBN;
-        num_m = WGRAD ? (p.M + 255) / 256 : 0;
+        num_m = WGRAD ? (p.M + TILE_M - 1) / TILE_M : 0;
         total = WGRAD ? p.E * num_m * num_n : g.tiles[p.E] * num_n;
     }
     // Within a group the row tiles run fastest: concurrent CTAs share the
@@ -51,14 +51,14 @@ struct GroupWalk {
         if constexpr (WGRAD) {
             const int per = num_m * num_n, i = t % per;
             r.e = t / per;
-            r.m0 = (i % num_m) * 256;
+            r.m0 = (i % num_m) * TILE_M;
             r.n0 = (i / num_m) * kGemmBN;
             r.k0 = g.padded[r.e];
             r.k = g.padded[r.e + 1] - r.k0;
         } else {
             r.e = group_of(g.tiles, p.E, t / num_n);
             const int first = g.tiles[r.e], tm = g.tiles[r.e + 1] - first, i = t - first * num_n;
-            r.m0 = (i % tm) * 256;
+            r.m0 = (i % tm) * TILE_M;
             r.n0 = (i / tm) * kGemmBN;
             r.k0 = 0;
             r.k = p.K;
@@ -209,7 +209,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     cluster_sync();  // barriers of both CTAs initialised, tensor memory allocated, groups known
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const GroupWalk<WGRAD> walk(groups, p);
+    const GroupWalk<WGRAD, 2 * BM> walk(groups, p);
 
     if (warp == 0) {
         // ---------------- TMA producer (both CTAs) ----------------
@@ -332,13 +332,217 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
 }
 
+// Few rows per group (the rows product alone): single CTAs on 128 x 256 tiles,
+// as the dense single-CTA kernel. A pair's second CTA would multiply rows that
+// are no group's, and there would be half as many tiles in flight.
+constexpr int GS_SMEM = SMEM_BYTES + (int)sizeof(GroupTable);
+static_assert(GS_SMEM <= 227 * 1024, "shared memory of one CTA");
+
+template <int FMT>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    gemm_grouped_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                               const GroupedParams p) {
+    constexpr int SF_K = (FMT == kNvfp4) ? 64 : 128;
+    constexpr int ATOMS_PER_KT = BK / SF_K;  // 4 or 2
+    extern __shared__ __align__(1024) uint8_t dyn_smem[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
+    uint8_t* sA = base;
+    uint8_t* sB = sA + STAGES * A_STAGE;
+    uint8_t* sSFA = sB + STAGES * B_STAGE;
+    uint8_t* sSFB = sSFA + STAGES * SFA_STAGE;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sSFB + STAGES * SFB_STAGE);
+    uint64_t* empty = full + STAGES;
+    uint64_t* sf_load = empty + STAGES;
+    uint64_t* sf_full = sf_load + STAGES;
+    uint64_t* acc_full = sf_full + STAGES;
+    uint64_t* acc_empty = acc_full + 1;
+    uint64_t* drain = acc_empty + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    GroupTable& groups = *reinterpret_cast<GroupTable*>(sSFB + STAGES * SFB_STAGE + 256);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int KT = (p.K + BK - 1) / BK;
+
+    if (threadIdx.x == 0) {
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmB);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+            mbar_init(&sf_load[s], 1);
+            mbar_init(&sf_full[s], kScaleWarps);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, kEpiWarps);
+        mbar_init(drain, 1);
+        fence_mbarrier_init();
+    }
+    if (warp == 0) tmem_alloc(tmem_slot, TMEM_COLS);
+    pdl_wait();  // the offsets and the operands are written (and the previous readers of D done)
+    pdl_launch_dependents();
+    if (warp == 1) build_groups(groups, p.offsets, p.E, p.T, BM, lane);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const GroupWalk<false, BM> walk(groups, p);
+
+    if (warp == 0) {
+        // ---------------- TMA producer ----------------
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < walk.total && ok; t += gridDim.x) {
+                const GroupTile w = walk.at(t);
+                const int arow = groups.padded[w.e] + w.m0, brow = w.e * p.b_rows + w.n0, bk0 = w.e * p.b_k;
+                const int nrb = (w.n0 + 128 < p.N) ? 2 : 1;  // B row blocks of this group
+                for (int kt = 0; kt < KT; ++kt, ++it) {
+                    const int s = it % STAGES;
+                    if (it >= STAGES && !mbar_wait(&empty[s], ((it / STAGES) + 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const int atoms = (min(BK, p.K - kt * BK) + SF_K - 1) / SF_K;
+                    mbar_arrive_expect_tx(&sf_load[s], atoms * 512 * (1 + nrb));
+                    const int64_t katom = (int64_t)kt * ATOMS_PER_KT;
+                    bulk_load(sSFA + s * SFA_STAGE, p.sfa + ((int64_t)(arow / 128) * p.atoms_a + katom) * 512, atoms * 512,
+                              &sf_load[s]);
+                    for (int rb = 0; rb < nrb; ++rb)
+                        bulk_load(sSFB + s * SFB_STAGE + rb * (ATOMS_PER_KT * 512),
+                                  p.sfb + ((int64_t)(brow / 128 + rb) * p.atoms_b + bk0 / SF_K + katom) * 512, atoms * 512,
+                                  &sf_load[s]);
+                    mbar_arrive_expect_tx(&full[s], A_STAGE + B_STAGE);
+                    tma_load_2d(sA + s * A_STAGE, &tmA, &full[s], kt * (BK / 2), arow);
+                    tma_load_2d(sB + s * B_STAGE, &tmB, &full[s], bk0 / 2 + kt * (BK / 2), brow);
+                }
+            }
+            drain_loads(full, sf_load, STAGES, it);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        if (lane == 0) {
+            const uint64_t a_desc0 = sw128_desc(smem_u32(sA)), b_desc0 = sw128_desc(smem_u32(sB));
+            int s = 0, lt = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < walk.total && ok; t += gridDim.x, ++lt) {
+                if (lt > 0 && !mbar_wait(acc_empty, (lt - 1) & 1)) break;
+                tc_fence_after();
+                for (int kt = 0; kt < KT; ++kt) {
+                    if (!mbar_wait(&sf_full[s], ph)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    mma_ktile<FMT, false, BM>(tmem + TMEM_D, a_desc0 + (uint64_t)(s * (A_STAGE >> 4)),
+                                              b_desc0 + (uint64_t)(s * (B_STAGE >> 4)), tmem + sfa_col(s),
+                                              tmem + sfb_col(s), min(BK, p.K - kt * BK) / 64, kt == 0);
+                    tc_commit(&empty[s]);
+                    if (++s == STAGES) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+                tc_commit(acc_full);
+            }
+            tc_commit(drain);
+            (void)mbar_wait(drain, 0);
+        }
+    } else if (warp < kFirstEpiWarp) {
+        // ---------------- scale writers ----------------
+        const uint32_t tmem_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < walk.total && ok; t += gridDim.x) {
+            for (int kt = 0; kt < KT; ++kt) {
+                if (!mbar_wait(&sf_load[s], ph)) {
+                    ok = false;
+                    break;
+                }
+                write_scales<ATOMS_PER_KT>(tmem_lane, s, smem_u32(sSFA + s * SFA_STAGE), smem_u32(sSFB + s * SFB_STAGE),
+                                           lane, warp & 3);
+                if (!mbar_wait(&full[s], ph)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sf_full[s]);
+                if (++s == STAGES) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+    } else {
+        // ---------------- epilogue: each lane stores its row ----------------
+        const int lq = warp & 3;
+        const int chalf = (warp - kFirstEpiWarp) >> 2;
+        const float scale = __fmul_rn(__ldg(p.ga), __ldg(p.gb));
+        int lt = 0;
+        for (int t = blockIdx.x; t < walk.total; t += gridDim.x, ++lt) {
+            const GroupTile w = walk.at(t);
+            if (!mbar_wait(acc_full, lt & 1)) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem + ((uint32_t)(lq * 32) << 16) + TMEM_D + chalf * 128;
+            const int m = w.m0 + lq * 32 + lane, n0 = w.n0 + chalf * 128;
+            const bool mine = m < groups.size(w.e);
+            const int64_t row = groups.row[w.e] + m;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t acc[64];
+                tmem_ld_32x32b_x32(taddr + 64 * h, acc);
+                tmem_ld_32x32b_x32(taddr + 64 * h + 32, acc + 32);
+                tc_wait_ld();
+                if (h == 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(acc_empty);
+                }
+                if (!mine) continue;
+                if (!p.out_f32) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) acc[c] = pack_bf16(acc[2 * c], acc[2 * c + 1], scale);
+                    store_row_words(p, acc, row, n0 + 64 * h);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) acc[c] = __float_as_uint(__fmul_rn(__uint_as_float(acc[c]), scale));
+                    store_row_words(p, acc, row, n0 + 64 * h);
+                    store_row_words(p, acc + 32, row, n0 + 64 * h + 32);
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+        tmem_relinquish();
+    }
+}
+
 }  // namespace
 
-cudaError_t launch_gemm_grouped(const GroupedParams& p, int fmt, bool wgrad, const CUtensorMap* tmapA,
+cudaError_t launch_gemm_grouped(const GroupedParams& p, int fmt, bool wgrad, bool pair, const CUtensorMap* tmapA,
                                 const CUtensorMap* tmapB, const CUtensorMap* tmapSFA, const CUtensorMap* tmapSFB,
                                 const CUtensorMap* tmapD, cudaStream_t s, int sms) {
     // the tile count is known on the device only: an upper bound sizes the grid
     const int64_t num_n = (p.N + kGemmBN - 1) / kGemmBN;
+    if (!pair) {
+        const int64_t tiles = std::min<int64_t>(p.T, p.T / 128 + p.E) * num_n;
+        auto run = [&](auto* kern) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GS_SMEM);
+            if (e != cudaSuccess) return e;
+            return launch_pdl(kern, dim3((unsigned)std::min<int64_t>(sms, tiles)), dim3(kGemmThreads), GS_SMEM, s, *tmapA,
+                              *tmapB, p);
+        };
+        const cudaError_t e = fmt == kNvfp4 ? run(gemm_grouped_single_kernel<kNvfp4>) : run(gemm_grouped_single_kernel<kMxfp4>);
+        count_launch();
+        return e;
+    }
     const int64_t num_m = wgrad ? (int64_t)p.E * ((p.M + 255) / 256) : std::min<int64_t>(p.T, p.T / 256 + p.E);
     const int clusters = (int)std::max<int64_t>(1, std::min<int64_t>(sms / 2, num_m * num_n));
     auto run = [&](auto* kern) {

@@ -17,7 +17,8 @@
 // or one warp; a thread holds 32 elements of it, whole Hadamard groups, so
 // that the rotation needs no shuffles. CTAs are persistent: the weight is
 // loaded once, and the next row's loads are issued before the row's sum is
-// joined.
+// joined. The backward pass of wide rows has them arrive through a ring in
+// shared memory.
 #include "qfp4_device.cuh"
 #include "qfp4_internal.h"
 
@@ -27,6 +28,8 @@ namespace {
 constexpr int kNormElems = 32;        // elements of a row per thread
 constexpr int kNormWarpRowC = 1024;   // up to this many columns a row belongs to one warp
 constexpr int kNormMaxThreads = 512;  // C <= 16384
+constexpr int kNormMaxStages = 4;     // rows in flight per CTA of the backward ring
+constexpr int kNormRingBytes = 192 * 1024;
 
 // A thread's 32 elements are NCH chunks of G consecutive ones (G = 16: chunks
 // t and t + threads per row; G = 32: chunk t).
@@ -198,68 +201,181 @@ __global__ void __launch_bounds__(WARP_ROW ? 128 : kNormMaxThreads) rmsnorm_fwd_
     }
 }
 
-// The rows' weight gradients stay in each thread's registers (32 columns) and
-// leave once per row owner, as row `owner` of p.dw_partials.
-template <bool WARP_ROW>
-__global__ void __launch_bounds__(WARP_ROW ? 128 : kNormMaxThreads) rmsnorm_bwd_kernel(const NormBwdParams p) {
-    using Chunks = NormChunks<16>;
-    __shared__ float red[2][kNormMaxThreads / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t owners = WARP_ROW ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
-    const int64_t first = WARP_ROW ? (int64_t)blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
-    const Chunks ch{WARP_ROW ? 32 : (int)blockDim.x, WARP_ROW ? lane : (int)threadIdx.x, (int)(p.C / 16)};
+// ---- backward ------------------------------------------------------------------
+// A thread holds up to NV chunks of eight columns (chunks t, t + threads, ...)
+// and keeps the weight gradient of its columns in registers over all its rows;
+// it leaves once per row owner, as row `owner` of p.dw_partials.
+template <int NV>
+struct NormBwdThread {
+    int t, threads, chunks;
+    float dw[8 * NV];
+    uint32_t ww[4 * NV];
+    __device__ __forceinline__ bool has(int i) const { return t + i * threads < chunks; }
+    __device__ __forceinline__ int at(int i) const { return 8 * (t + i * threads); }
+    __device__ __forceinline__ void load(const uint16_t* row, uint32_t* w) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            uint4 q = make_uint4(0, 0, 0, 0);
+            if (has(i)) q = *reinterpret_cast<const uint4*>(row + at(i));
+            w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
+        }
+    }
+    __device__ __forceinline__ void init(const NormBwdParams& p, int t_, int threads_) {
+        t = t_;
+        threads = threads_;
+        chunks = (int)(p.C / 8);
+        load(p.w, ww);
+#pragma unroll
+        for (int i = 0; i < 8 * NV; ++i) dw[i] = 0.0f;
+    }
+    // This thread's part of sum g h rstd.
+    __device__ __forceinline__ float dot(const uint32_t* dy, const uint32_t* h, float rstd) const {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4 * NV; ++i) {
+            s = __fmaf_rn(__fmul_rn(bf16lo(dy[i]), bf16lo(ww[i])), __fmul_rn(bf16lo(h[i]), rstd), s);
+            s = __fmaf_rn(__fmul_rn(bf16hi(dy[i]), bf16hi(ww[i])), __fmul_rn(bf16hi(h[i]), rstd), s);
+        }
+        return s;
+    }
+    // dx of the row (c = the row's sum / C) and its share of dw.
+    __device__ __forceinline__ void finish(const NormBwdParams& p, int64_t row, const uint32_t* dy, const uint32_t* h,
+                                           const uint32_t* dh, float rstd, float c) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            uint32_t out[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = 4 * i + j;
+                float d[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const float dyv = b ? bf16hi(dy[k]) : bf16lo(dy[k]);
+                    const float hr = __fmul_rn(b ? bf16hi(h[k]) : bf16lo(h[k]), rstd);
+                    dw[2 * k + b] = __fmaf_rn(dyv, hr, dw[2 * k + b]);
+                    const float v = __fmaf_rn(-hr, c, __fmul_rn(dyv, b ? bf16hi(ww[k]) : bf16lo(ww[k])));
+                    d[b] = p.dh != nullptr ? __fmaf_rn(rstd, v, b ? bf16hi(dh[k]) : bf16lo(dh[k])) : __fmul_rn(rstd, v);
+                }
+                out[j] = norm_pack(d[0], d[1]);
+            }
+            if (has(i))
+                *chk(reinterpret_cast<uint4*>(p.dx + row * p.lddx + at(i)), p.dx, rows_extent(p.R, p.C, p.lddx)) =
+                    make_uint4(out[0], out[1], out[2], out[3]);
+        }
+    }
+    __device__ __forceinline__ void write_dw(const NormBwdParams& p, int64_t owner, int64_t owners) const {
+#pragma unroll
+        for (int i = 0; i < 2 * NV; ++i)
+            if (has(i / 2))
+                *chk(reinterpret_cast<float4*>(p.dw_partials + owner * p.C + at(i / 2) + 4 * (i & 1)), p.dw_partials,
+                     owners * p.C * 4) = make_float4(dw[4 * i], dw[4 * i + 1], dw[4 * i + 2], dw[4 * i + 3]);
+    }
+};
+
+// C <= 512: a row belongs to one warp, loads straight to registers, the next
+// row's before this row's sum is joined.
+template <int NV>
+__global__ void __launch_bounds__(128, 4) rmsnorm_bwd_warp_kernel(const NormBwdParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t owners = (int64_t)gridDim.x * 4, first = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     pdl_wait();
     pdl_launch_dependents();
-    uint32_t ww[16];
-    ch.load(p.w, ww);
-    float dw[kNormElems];
+    NormBwdThread<NV> th;
+    th.init(p, lane, 32);
+    uint32_t dy[4 * NV], h[4 * NV], dh[4 * NV], dy1[4 * NV], h1[4 * NV], dh1[4 * NV];
+    float rstd = 0.0f, rstd1 = 0.0f;
+    auto fetch = [&](int64_t row) {
+        th.load(p.dy + row * p.lddy, dy1);
+        th.load(p.h + row * p.ldh, h1);
+        if (p.dh != nullptr) th.load(p.dh + row * p.lddh, dh1);
+        rstd1 = p.rstd[row];
+    };
+    if (first < p.R) fetch(first);
+    for (int64_t row = first; row < p.R; row += owners) {
 #pragma unroll
-    for (int i = 0; i < kNormElems; ++i) dw[i] = 0.0f;
-    int parity = 0;
-    for (int64_t row = first; row < p.R; row += owners, parity ^= 1) {
-        uint32_t dyw[16], hw[16], dhw[16];
-        ch.load(p.dy + row * p.lddy, dyw);
-        ch.load(p.h + row * p.ldh, hw);
-        const float rstd = p.rstd[row];
-        if (p.dh != nullptr) ch.load(p.dh + row * p.lddh, dhw);
-        float dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            dot = __fmaf_rn(__fmul_rn(bf16lo(dyw[i]), bf16lo(ww[i])), __fmul_rn(bf16lo(hw[i]), rstd), dot);
-            dot = __fmaf_rn(__fmul_rn(bf16hi(dyw[i]), bf16hi(ww[i])), __fmul_rn(bf16hi(hw[i]), rstd), dot);
+        for (int i = 0; i < 4 * NV; ++i) {
+            dy[i] = dy1[i];
+            h[i] = h1[i];
+            dh[i] = dh1[i];
         }
-        const float c = __fmul_rn(norm_row_sum<WARP_ROW>(dot, red, parity), p.inv_c);
+        rstd = rstd1;
+        if (row + owners < p.R) fetch(row + owners);
+        float s = th.dot(dy, h, rstd);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float d[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float dy = k ? bf16hi(dyw[i]) : bf16lo(dyw[i]);
-                const float w = k ? bf16hi(ww[i]) : bf16lo(ww[i]);
-                const float hr = __fmul_rn(k ? bf16hi(hw[i]) : bf16lo(hw[i]), rstd);
-                dw[2 * i + k] = __fmaf_rn(dy, hr, dw[2 * i + k]);
-                const float t = __fmaf_rn(-hr, c, __fmul_rn(dy, w));
-                d[k] = p.dh != nullptr ? __fmaf_rn(rstd, t, k ? bf16hi(dhw[i]) : bf16lo(dhw[i])) : __fmul_rn(rstd, t);
-            }
-            dyw[i] = norm_pack(d[0], d[1]);
-        }
-        ch.store(p.dx + row * p.lddx, dyw, p.dx, rows_extent(p.R, p.C, p.lddx));
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        th.finish(p, row, dy, h, dh, rstd, __fmul_rn(s, p.inv_c));
     }
+    th.write_dw(p, first, owners);
+}
+
+// C > 512: a row belongs to one CTA of C / 16 threads. Rows arrive by bulk
+// copies into a ring of p.stages shared-memory stages (dy, h and, if given, dh of
+// one row each), so that several rows per SM are in flight without registers
+// to hold them: measured on 16384 x 4096, 187 us with the rows loaded to
+// registers when they are due, see the host code for the figure with the ring.
+template <int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS) rmsnorm_bwd_ring_kernel(const NormBwdParams p) {
+    extern __shared__ __align__(1024) uint8_t dyn_smem[];
+    __shared__ uint64_t full[kNormMaxStages];
+    __shared__ float red[2][32];
+    __shared__ int dead;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const uint32_t row_bytes = (uint32_t)p.C * 2, parts = p.dh != nullptr ? 3 : 2;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
+        fence_mbarrier_init();
+        dead = 0;
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
+    auto fetch = [&](int64_t row, int s) {  // one thread
+        uint8_t* d = dyn_smem + s * parts * row_bytes;
+        mbar_arrive_expect_tx(&full[s], parts * row_bytes);
+        bulk_load(d, p.dy + row * p.lddy, row_bytes, &full[s]);
+        bulk_load(d + row_bytes, p.h + row * p.ldh, row_bytes, &full[s]);
+        if (p.dh != nullptr) bulk_load(d + 2 * row_bytes, p.dh + row * p.lddh, row_bytes, &full[s]);
+    };
+    if (threadIdx.x == 0)
+        for (int s = 0; s < p.stages && blockIdx.x + (int64_t)s * gridDim.x < p.R; ++s)
+            fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+    NormBwdThread<NV> th;
+    th.init(p, threadIdx.x, blockDim.x);
+    float rstd1 = blockIdx.x < p.R ? p.rstd[blockIdx.x] : 0.0f;
+    int s = 0, parity = 0;
+    uint32_t phase = 0;
+    for (int64_t row = blockIdx.x; row < p.R; row += gridDim.x, parity ^= 1) {
+        const float rstd = rstd1;
+        if (row + gridDim.x < p.R) rstd1 = p.rstd[row + gridDim.x];
+        if (!mbar_wait(&full[s], phase)) dead = 1;  // seen by all behind the barrier
+        const uint16_t* d = reinterpret_cast<const uint16_t*>(dyn_smem + s * parts * row_bytes);
+        uint32_t dy[4 * NV], h[4 * NV], dh[4 * NV];
+        th.load(d, dy);
+        th.load(d + p.C, h);
+        if (p.dh != nullptr) th.load(d + 2 * p.C, dh);
+        float sum = th.dot(dy, h, rstd);
 #pragma unroll
-    for (int i = 0; i < Chunks::NCH; ++i)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-            if (ch.has(i))
-                *chk(reinterpret_cast<float4*>(p.dw_partials + first * p.C + ch.at(i) + 4 * v), p.dw_partials,
-                     owners * p.C * 4) = make_float4(dw[16 * i + 4 * v], dw[16 * i + 4 * v + 1],
-                                                     dw[16 * i + 4 * v + 2], dw[16 * i + 4 * v + 3]);
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) red[parity][warp] = sum;
+        __syncthreads();  // the sums are written, and the stage is read
+        if (dead) break;
+        if (threadIdx.x == 0 && row + (int64_t)p.stages * gridDim.x < p.R) fetch(row + (int64_t)p.stages * gridDim.x, s);
+        sum = red[parity][0];
+        for (int w = 1; w < warps; ++w) sum += red[parity][w];
+        th.finish(p, row, dy, h, dh, rstd, __fmul_rn(sum, p.inv_c));
+        if (++s == p.stages) {
+            s = 0;
+            phase ^= 1u;
+        }
+    }
+    th.write_dw(p, blockIdx.x, gridDim.x);
 }
 
 // dw[c] (+)= the sum of column c of the n partial rows, in a fixed order: 32
-// columns per CTA, eight threads per column.
-__global__ void __launch_bounds__(256) norm_dw_reduce_kernel(const float* partials, int n, int64_t C, float* dw,
-                                                             int accumulate) {
-    __shared__ float red[8][33];
+// columns per CTA, 32 threads per column.
+__global__ void __launch_bounds__(1024) norm_dw_reduce_kernel(const float* partials, int n, int64_t C, float* dw,
+                                                              int accumulate) {
+    __shared__ float red[32][33];
     const int col = threadIdx.x & 31, part = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + col;
     pdl_wait();
@@ -267,15 +383,16 @@ __global__ void __launch_bounds__(256) norm_dw_reduce_kernel(const float* partia
     float s = 0.0f;
     if (c < C) {
 #pragma unroll 8
-        for (int r = part; r < n; r += 8) s += partials[(int64_t)r * C + c];
+        for (int r = part; r < n; r += 32) s += partials[(int64_t)r * C + c];
     }
     red[part][col] = s;
     __syncthreads();
-    if (part == 0 && c < C) {
+    // warp w joins column w's 32 parts
+    s = red[col][part];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += red[i][col];
-        *chk(dw + c, dw, C * 4) = accumulate ? __fadd_rn(dw[c], s) : s;
-    }
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int64_t cw = (int64_t)blockIdx.x * 32 + part;
+    if (col == 0 && cw < C) *chk(dw + cw, dw, C * 4) = accumulate ? __fadd_rn(dw[cw], s) : s;
 }
 
 // Threads of a CTA and CTAs for R rows of C columns: as many as the SMs hold
@@ -327,16 +444,33 @@ cudaError_t launch_rmsnorm_fwd(NormParams p, int nh, bool quant, float* amax, in
 
 int64_t norm_bwd_partial_rows(int64_t R) { return std::min<int64_t>((R + 3) / 4 * 4, kMaxNormPartials); }
 
-cudaError_t launch_rmsnorm_bwd(const NormBwdParams& p, float* dw, int accumulate, int sms, cudaStream_t s) {
-    int threads = 0, grid = 0;
-    norm_grid(p.R, p.C, sms, kMaxNormPartials, &threads, &grid);
-    const bool warp_row = p.C <= kNormWarpRowC;
-    cudaError_t e = warp_row ? launch_pdl(rmsnorm_bwd_kernel<true>, dim3(grid), dim3(threads), 0, s, p)
-                             : launch_pdl(rmsnorm_bwd_kernel<false>, dim3(grid), dim3(threads), 0, s, p);
+cudaError_t launch_rmsnorm_bwd(NormBwdParams p, float* dw, int accumulate, int sms, cudaStream_t s) {
+    cudaError_t e;
+    int owners;
+    if (p.C <= 512) {
+        const int grid = (int)std::min<int64_t>((p.R + 3) / 4, std::min(4 * sms, kMaxNormPartials / 4));
+        owners = 4 * grid;
+        auto run = [&](auto* kern) { return launch_pdl(kern, dim3(grid), dim3(128), 0, s, p); };
+        e = p.C <= 256 ? run(rmsnorm_bwd_warp_kernel<1>)
+                       : run(rmsnorm_bwd_warp_kernel<2>);
+    } else {
+        // 512 threads per SM, and its shared memory shared out among their rings
+        const int threads = (int)((p.C + 511) / 512 * 32);
+        const int per_sm = std::max(1, 512 / threads);
+        const int stage = (p.dh != nullptr ? 3 : 2) * (int)p.C * 2;
+        p.stages = std::min(kNormMaxStages, kNormRingBytes / per_sm / stage);
+        owners = (int)std::min<int64_t>(p.R, std::min(per_sm * sms, kMaxNormPartials));
+        auto run = [&](auto* kern) {
+            const cudaError_t a = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRingBytes);
+            if (a != cudaSuccess) return a;
+            return launch_pdl(kern, dim3(owners), dim3(threads), (size_t)(p.stages * stage), s, p);
+        };
+        e = threads <= 512 ? run(rmsnorm_bwd_ring_kernel<2, 512>) : run(rmsnorm_bwd_ring_kernel<2, 1024>);
+    }
     count_launch();
     if (e != cudaSuccess) return e;
-    e = launch_pdl(norm_dw_reduce_kernel, dim3((unsigned)((p.C + 31) / 32)), dim3(256), 0, s,
-                   static_cast<const float*>(p.dw_partials), warp_row ? 4 * grid : grid, p.C, dw, accumulate);
+    e = launch_pdl(norm_dw_reduce_kernel, dim3((unsigned)((p.C + 31) / 32)), dim3(1024), 0, s,
+                   static_cast<const float*>(p.dw_partials), owners, p.C, dw, accumulate);
     count_launch();
     return e;
 }

@@ -192,22 +192,6 @@ int make_row_tmap(CUtensorMap* tm, const void* x, int64_t R, int64_t C, int64_t 
     return QFP4_OK;
 }
 
-// 2-D view of a bf16 R x C tensor for gathered rows: box 64 columns x 1 row
-// (128 bytes), 128-byte swizzle.
-int make_gather_tmap(CUtensorMap* tm, const void* x, int64_t R, int64_t C, int64_t ld) {
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return cuda_fail(cudaErrorNotSupported);
-    const cuuint64_t dims[2] = {(cuuint64_t)C, (cuuint64_t)R};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {64, 1};
-    const cuuint32_t estr[2] = {1, 1};
-    CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(x), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
-    return QFP4_OK;
-}
-
 // Rows in groups: x has T rows; the R (or k) rows that a quantizer counts are
 // those of the padded layout (see include/qfp4.h).
 struct Groups {
@@ -220,6 +204,47 @@ void set_groups(QuantParams& p, const Groups* gr) {
     p.group_offsets = gr->offsets;
     p.groups = gr->E;
     p.group_T = (int)gr->T;
+}
+
+// The two TMA views of x (T x C) for a pass over rows in groups.
+// tm[0], boxes of consecutive rows from any row on: along ROW a 2-D view, box
+// 64 columns x 128 rows; along COL 5-D views whose last dimension is the first
+// row (a box starts so that it ends inside x, its rows are offsets from there):
+// the bands' (column, r % 2, r / 64 % 2, r / 2 % 32, first row) for G = 0, else
+// (column, r % 2, r / G, r / 2 % (G / 2), first row) of 4 G rows.
+// tm[1], single rows for gathering: box 64 columns x 1 row.
+// 128-byte swizzle in both.
+int make_group_tmaps(CUtensorMap* tm, const void* x, int64_t T, int64_t C, int64_t ld, int axis, int G) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return cuda_fail(cudaErrorNotSupported);
+    const auto encode = [&](CUtensorMap* m, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                            const cuuint32_t* box) {
+        const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+        return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(x), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    const cuuint64_t row = (cuuint64_t)ld * 2;
+    const cuuint64_t dims2[2] = {(cuuint64_t)C, (cuuint64_t)T};
+    const cuuint32_t box1[2] = {64, 1}, box128[2] = {64, 128};
+    bool ok = encode(&tm[1], 2, dims2, &row, box1);
+    const int64_t rows = G > 0 ? 4 * G : 128;  // of a box
+    if (axis == QFP4_AXIS_ROW) {
+        ok = ok && encode(&tm[0], 2, dims2, &row, box128);
+    } else if (T < rows) {
+        tm[0] = tm[1];  // no box lies inside x: every row is gathered
+    } else if (G == 0) {
+        const cuuint64_t dims[5] = {(cuuint64_t)C, 2, 2, 32, (cuuint64_t)(T - rows + 1)};
+        const cuuint64_t strides[4] = {row, 64 * row, 2 * row, row};
+        const cuuint32_t box[5] = {64, 2, 2, 32, 1};
+        ok = ok && encode(&tm[0], 5, dims, strides, box);
+    } else {
+        const cuuint64_t dims[5] = {(cuuint64_t)C, 2, 4, (cuuint64_t)(G / 2), (cuuint64_t)(T - rows + 1)};
+        const cuuint64_t strides[4] = {row, (cuuint64_t)G * row, 2 * row, row};
+        const cuuint32_t box[5] = {64, 2, 4, (cuuint32_t)(G / 2), 1};
+        ok = ok && encode(&tm[0], 5, dims, strides, box);
+    }
+    return ok ? QFP4_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
 // TMA view of x for a pass in the given orientation (G: column-mode group).
@@ -372,11 +397,11 @@ int run_amax(const void* x, int64_t R, int64_t C, int64_t ld, int32_t had, int32
     p.amax_out = partials;
     const int nh = had_n(had);
     const int G = col_group(16, nh);
-    CUtensorMap tm;
-    int rc = gr ? make_gather_tmap(&tm, x, gr->T, C, ld) : make_input_tmap(&tm, x, R, C, ld, axis, G);
+    CUtensorMap tm[2];
+    int rc = gr ? make_group_tmaps(tm, x, gr->T, C, ld, axis, G) : make_input_tmap(tm, x, R, C, ld, axis, G);
     if (rc) return rc;
     *n_partials = amax_partial_count(sms, quant_tiles(axis, g.rows, g.k, G));
-    cudaError_t e = launch_amax(p, axis, nh, &tm, *n_partials, s);
+    cudaError_t e = launch_amax(p, axis, nh, tm, *n_partials, s);
     return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
 }
 
@@ -483,16 +508,16 @@ int quantize_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t fmt, 
         p.amax_partials = partials;
         p.n_partials = n;
     }
-    CUtensorMap tm;
+    CUtensorMap tm[2];
     if (gr != nullptr)
-        rc = make_gather_tmap(&tm, x, gr->T, C, ld);
+        rc = make_group_tmaps(tm, x, gr->T, C, ld, axis, 0);
     else if (bands)
-        rc = make_col64_tmap(&tm, x, R, C, ld);
+        rc = make_col64_tmap(tm, x, R, C, ld);
     else
-        rc = make_input_tmap(&tm, x, R, C, ld, axis, col_group(NB, nh));
+        rc = make_input_tmap(tm, x, R, C, ld, axis, col_group(NB, nh));
     if (rc) return rc;
-    cudaError_t e = fused ? launch_quant_fused(p, rounding, nh, bands ? 2 : axis, &tm, s)
-                          : launch_quant(p, sfmt, rounding, nh, bands ? 2 : axis, &tm, s);
+    cudaError_t e = fused ? launch_quant_fused(p, rounding, nh, bands ? 2 : axis, tm, s)
+                          : launch_quant(p, sfmt, rounding, nh, bands ? 2 : axis, tm, s);
     return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
 }
 
@@ -565,10 +590,11 @@ int quantize_dual_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t 
     p.sr_seed_row = seed_row->sr;
     p.sr_tag_elem_row = (uint32_t)kTagElement | (seed_row->sr_stream << 4);
     p.sr_tag_scale_row = (uint32_t)kTagScale | (seed_row->sr_stream << 4);
-    CUtensorMap tm;
-    if ((rc = gr ? make_gather_tmap(&tm, x, gr->T, C, ld) : make_col64_tmap(&tm, x, R, C, ld))) return rc;
+    CUtensorMap tm[2];
+    if ((rc = gr ? make_group_tmaps(tm, x, gr->T, C, ld, QFP4_AXIS_COL, 0) : make_col64_tmap(tm, x, R, C, ld)))
+        return rc;
     const int sfmt = (fmt == QFP4_MXFP4_RU) ? QFP4_MXFP4 : fmt;
-    cudaError_t e = launch_quant_dual(p, sfmt, rounding, had_n(had_col), had_n(had_row), &tm, s);
+    cudaError_t e = launch_quant_dual(p, sfmt, rounding, had_n(had_col), had_n(had_row), tm, s);
     return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
 }
 
@@ -823,13 +849,14 @@ int amax_rowcol_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t ha
         if (2 * n > kMaxAmaxPartials) return QFP4_ERR_WORKSPACE;
         p.amax_out = partials;
         p.amax_out_row = partials + n;
-        CUtensorMap tm;
+        CUtensorMap tm[2];
         if (bands) {
-            if ((rc = gr ? make_gather_tmap(&tm, x, gr->T, C, ld) : make_col64_tmap(&tm, x, R, C, ld))) return rc;
-            e = launch_amax_rowcol64(p, nh, &tm, n, s);
+            if ((rc = gr ? make_group_tmaps(tm, x, gr->T, C, ld, QFP4_AXIS_COL, 0) : make_col64_tmap(tm, x, R, C, ld)))
+                return rc;
+            e = launch_amax_rowcol64(p, nh, tm, n, s);
         } else {
-            if ((rc = make_input_tmap(&tm, x, R, C, ld, QFP4_AXIS_COL, 16))) return rc;
-            e = launch_amax_rowcol(p, nh, &tm, n, s);
+            if ((rc = make_input_tmap(tm, x, R, C, ld, QFP4_AXIS_COL, 16))) return rc;
+            e = launch_amax_rowcol(p, nh, tm, n, s);
         }
         if (e == cudaSuccess) e = launch_reduce_max(partials, n, amax_col, s);
         if (e == cudaSuccess) e = launch_reduce_max(partials + n, n, amax_row, s);
@@ -1218,14 +1245,20 @@ int run_grouped(const qfp4_tensor* A, const qfp4_tensor* B, bool wgrad, int64_t 
     const auto atoms_k = [&](int64_t k) { return (k / NB + 3) / 4; };
     p.ga = A->tensor_scale;
     p.gb = B->tensor_scale;
+    p.sfa = A->scales;
+    p.sfb = B->scales;
+    p.atoms_a = (int)atoms_k(A->k);
+    p.atoms_b = (int)atoms_k(B->k);
+    // as the dense GEMM: pairs unless the groups have at most 128 rows, here on average
+    const bool pair = wgrad || use_pair_gemm(p.T / p.E);
     CUtensorMap tA, tB, tSFA, tSFB, tD;
     int rc;
     if ((rc = make_codes_tmap(&tA, A->codes, A->rows, A->k, kGemmBM))) return rc;
-    if ((rc = make_codes_tmap(&tB, B->codes, B->rows, B->k, 128))) return rc;
+    if ((rc = make_codes_tmap(&tB, B->codes, B->rows, B->k, pair ? 128 : kGemmBN))) return rc;
     if ((rc = make_scale_tmap(&tSFA, A->scales, A->rows, atoms_k(A->k), apk, 1))) return rc;
     if ((rc = make_scale_tmap(&tSFB, B->scales, B->rows, atoms_k(B->k), apk, 2))) return rc;
     if ((rc = make_out_tmap(&tD, p.D, d_rows, p.N, p.ldd, p.out_f32))) return rc;
-    const cudaError_t e = launch_gemm_grouped(p, A->fmt, wgrad, &tA, &tB, &tSFA, &tSFB, &tD, s, sms);
+    const cudaError_t e = launch_gemm_grouped(p, A->fmt, wgrad, pair, &tA, &tB, &tSFA, &tSFB, &tD, s, sms);
     return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
 }
 
@@ -1242,7 +1275,7 @@ int gemm_grouped_impl(const qfp4_tensor* A, const qfp4_tensor* B, const int32_t*
     const int64_t N = by_rows ? B->rows / E : B->rows;
     if (by_rows ? B->rows % E != 0 : B->k != K * E) return QFP4_ERR_INVALID_ARG;
     if (N % 8 != 0 || (E > 1 && (by_rows ? N : K) % 128 != 0)) return QFP4_ERR_INVALID_ARG;
-    if ((T / 256 + E) * ((N + kGemmBN - 1) / kGemmBN) > 0x7fffffffLL) return QFP4_ERR_INVALID_ARG;
+    if ((T / 128 + E) * ((N + kGemmBN - 1) / kGemmBN) > 0x7fffffffLL) return QFP4_ERR_INVALID_ARG;
     if (T == 0 || N == 0) return QFP4_OK;
     const int64_t esz = out_dtype == QFP4_OUT_F32 ? 4 : 2;
     if (D == nullptr || ldd < N) return QFP4_ERR_INVALID_ARG;

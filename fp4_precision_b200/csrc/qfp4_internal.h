@@ -56,9 +56,8 @@ struct QuantParams {
     // and are read back through amax_partials.
     uint32_t* grid_counter;
     // Rows in groups (nullptr: none): x then has group_T rows in `groups`
-    // groups, and R (and so rows or k) counts those of the padded layout. tmap
-    // is the 2-D view whose boxes are one row high; the rows of a tile are
-    // gathered.
+    // groups, and R (and so rows or k) counts those of the padded layout; tmap
+    // points to two maps (GroupMaps in quant.cu).
     const int* group_offsets;
     int groups, group_T;
 };
@@ -172,6 +171,7 @@ struct NormBwdParams {
     uint16_t* dx;
     int64_t lddx;
     float* dw_partials;  // one row of C per row owner
+    int stages;          // of the ring (set by the launcher)
 };
 // At most this many rows of weight-gradient partials (four row owners per SM).
 constexpr int kMaxNormPartials = 592;
@@ -181,7 +181,7 @@ constexpr int kMaxNormPartials = 592;
 cudaError_t launch_rmsnorm_fwd(NormParams p, int nh, bool quant, float* amax, int sms, int* n_partials,
                                cudaStream_t s);
 int64_t norm_bwd_partial_rows(int64_t R);
-cudaError_t launch_rmsnorm_bwd(const NormBwdParams& p, float* dw, int accumulate, int sms, cudaStream_t s);
+cudaError_t launch_rmsnorm_bwd(NormBwdParams p, float* dw, int accumulate, int sms, cudaStream_t s);
 
 // grouped_sm100.cu: rows in groups (the experts of a mixture). offsets: device
 // int32 [E + 1], group e's rows are [offsets[e], offsets[e + 1]) of T; in the
@@ -200,10 +200,15 @@ struct GroupedParams {
     // e * b_rows and at element e * b_k of the reduction axis
     int M, N, K;
     int b_rows, b_k;
+    // the single-CTA kernel: the operands' scales and their atoms per 128-row block
+    const uint8_t* sfa;
+    const uint8_t* sfb;
+    int atoms_a, atoms_b;
 };
 // wgrad: the reduction runs over the groups' rows (D [E M x N]); else over K,
-// with the groups along the rows of A and D.
-cudaError_t launch_gemm_grouped(const GroupedParams& p, int fmt, bool wgrad, const CUtensorMap* tmapA,
+// with the groups along the rows of A and D, and by single CTAs with pair =
+// false (tmapB then has boxes of 256 rows; the last three maps are not read).
+cudaError_t launch_gemm_grouped(const GroupedParams& p, int fmt, bool wgrad, bool pair, const CUtensorMap* tmapA,
                                 const CUtensorMap* tmapB, const CUtensorMap* tmapSFA, const CUtensorMap* tmapSFB,
                                 const CUtensorMap* tmapD, cudaStream_t s, int sms);
 void count_launch();

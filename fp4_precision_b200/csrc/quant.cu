@@ -27,6 +27,8 @@
 // stride, written out as __fmaf_rn / __ffma2_rn; the library is built with
 // --fmad=false, and packed f32x2 operations round each lane like the scalar
 // instruction), so codes and scales are exactly those of the definition.
+#include <type_traits>
+
 #include "groups.cuh"
 #include "qfp4_device.cuh"
 #include "qfp4_internal.h"
@@ -771,79 +773,122 @@ __device__ __forceinline__ void ring_init(Ring<STAGES>& ring) {
 }
 
 // ---------------------------------------------------------------------------
-// Rows in groups: the tile's rows are those of the padded layout, gathered from
-// the groups' own rows by TMA (four per instruction, any rows); a row that is
-// no group's is read past the tensor and so zero. Only the producer differs:
-// the compute warps see a tile of the padded matrix. The kernels take this as a
-// template flag: as a branch at run time it cost the kernels without groups 1 %. One instruction per 512
-// bytes instead of one per tile, issued by the whole producer warp.
-
-// x-row (within the tile) that shared-memory row s holds.
-struct RowOrder {
-    __device__ static int row(int s) { return s; }
+// Rows in groups: a tile holds rows of the padded layout in segments of 128 (or
+// of the tile's, if fewer), each within one group or no group's. The producer
+// loads a segment from the group's own rows, which start at any row of x: one
+// box of consecutive rows, the first row as a coordinate of its own (a map
+// dimension of one row's stride that the box crosses nowhere). Rows behind the
+// group's end arrive as whatever follows them and are masked by the compute
+// warps, which know each segment's row count; a segment without rows is not
+// loaded. Where the box would leave x the rows are gathered one by one, rows
+// past x as zeros. (Gathering every segment measured 49 cycles per instruction
+// of 512 bytes, half the speed at which HBM delivers.) The kernels take all
+// this as a template flag: as a branch at run time it cost the kernels without
+// groups 1 %.
+struct GroupMaps {
+    CUtensorMap box, gather;
 };
-struct BandOrder {  // 64-row bands
-    __device__ static int row(int s) { return (s & 1) + 2 * (s >> 3) + 64 * ((s >> 1) & 3); }
+template <bool GROUPED>
+using TileMap = std::conditional_t<GROUPED, GroupMaps, CUtensorMap>;
+
+// Row of the segment that its shared-memory row u holds.
+struct RowOrder {
+    __device__ static int row(int u) { return u; }
+};
+struct BandOrder {  // two 64-row bands
+    __device__ static int row(int u) { return (u & 1) + 2 * (u >> 2) + 64 * ((u >> 1) & 1); }
 };
 template <int G>
-struct ColOrder {
-    __device__ static int row(int s) { return (s & 1) + 2 * ((s >> 3) & 3) + 8 * (s >> 5) + G * ((s >> 1) & 3); }
+struct ColOrder {  // four groups of G rows
+    __device__ static int row(int u) { return (u & 1) + 2 * (u >> 3) + G * ((u >> 1) & 3); }
 };
+// Shared-memory rows from one 128-row segment of a band tile to the next: the
+// four rows between them give the 8 rows of a transposing load (four bands,
+// two rows each) eight different places in the swizzle pattern.
+constexpr int kBandSegPitch = 132;
 
-// The table and, per ring stage, the rows that groups have in each 128-row
-// half of the tile; behind the ring in dynamic shared memory.
+// The table and, per ring stage, the rows that the tile's segments hold; behind
+// the ring in dynamic shared memory.
 template <int STAGES>
 struct GroupSmem {
     GroupTable table;
     int rows[STAGES][2];
 };
 
-// The producer warp of a kernel whose tiles are ROWS x (64 BOXES).
-template <int STAGES, int ROWS, int BOXES, typename Order>
-__device__ __forceinline__ void gather_tiles(const void* tmap, const int* offsets, int groups, int T, Ring<STAGES>& ring,
-                                          uint8_t* tiles, int tiles_c, int tiles_r, int lane) {
-    GroupSmem<STAGES>& gs = *reinterpret_cast<GroupSmem<STAGES>*>(tiles + STAGES * BOXES * ROWS * 128);
-    constexpr int BOX_BYTES = ROWS * 128;
-    build_groups(gs.table, offsets, groups, T, 128, lane);
+// The producer warp: tiles of SEGS segments of SEG_ROWS x (64 BOXES), a
+// segment's boxes SEG_ROWS and the segments PITCH shared-memory rows apart.
+template <int STAGES, int SEGS, int SEG_ROWS, int PITCH, int BOXES, int STAGE_BYTES, typename Order>
+__device__ __forceinline__ void load_group_tiles(const GroupMaps& maps, const QuantParams& p, Ring<STAGES>& ring,
+                                                 uint8_t* tiles, int tiles_c, int tiles_r, int lane) {
+    static_assert(SEGS == 1 || BOXES == 1, "one of the two");
+    constexpr bool kRow = std::is_same_v<Order, RowOrder>;
+    GroupSmem<STAGES>& gs = *reinterpret_cast<GroupSmem<STAGES>*>(tiles + STAGES * STAGE_BYTES);
+    build_groups(gs.table, p.group_offsets, p.groups, p.group_T, 128, lane);
     __syncwarp();
     int i = 0;
     for (TileWalk<STAGES> w(tiles_c); w.tr < tiles_r; w.next(), ++i) {
         const int s = w.stage;
         const bool ok = i < STAGES || mbar_wait(&ring.empty[s], w.phase ^ 1u);
         if (!__all_sync(0xffffffffu, ok)) break;
-        int src = 0, n = 0;  // lanes 0 and 1: first source row of the half, its rows
-        if (lane < (ROWS + 127) / 128) {
-            const int r = w.tr * ROWS + lane * 128;
-            const int e = group_of(gs.table.padded, groups, r);
+        int src = 0, n = 0;  // lane h: segment h's first source row, its rows
+        if (lane < SEGS) {
+            const int r = (w.tr * SEGS + lane) * SEG_ROWS;
+            const int e = group_of(gs.table.padded, p.groups, r);
             if (e >= 0) {
                 const int at = r - gs.table.padded[e];
                 src = gs.table.row[e] + at;
-                n = min(128, max(0, gs.table.size(e) - at));
+                n = min(SEG_ROWS, max(0, gs.table.size(e) - at));
             }
             gs.rows[s][lane] = n;
         }
-        const int src0 = __shfl_sync(0xffffffffu, src, 0), src1 = __shfl_sync(0xffffffffu, src, 1);
-        const int n0 = __shfl_sync(0xffffffffu, n, 0), n1 = __shfl_sync(0xffffffffu, n, 1);
-        if (lane == 0) mbar_arrive_expect_tx(&ring.full[s], BOXES * BOX_BYTES);
+        const uint32_t loaded = __ballot_sync(0xffffffffu, n > 0);  // segments with rows
+        __syncwarp();  // the counts are written before lane 0 arrives
+        if (lane == 0) {
+            if (loaded != 0)
+                mbar_arrive_expect_tx(&ring.full[s], __popc(loaded) * BOXES * SEG_ROWS * 128);
+            else
+                mbar_arrive(&ring.full[s]);
+        }
         __syncwarp();
 #pragma unroll
-        for (int s0 = 0; s0 < ROWS; s0 += 128) {
-            const int s4 = s0 + 4 * lane;
-            if (s4 < ROWS) {
-                int y[4];
+        for (int h = 0; h < SEGS; ++h) {
+            const int src_h = __shfl_sync(0xffffffffu, src, h), n_h = __shfl_sync(0xffffffffu, n, h);
+            if (n_h == 0) continue;
+            uint8_t* seg = tiles + s * STAGE_BYTES + h * PITCH * 128;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = Order::row(s4 + j), at = r & 127;
-                    y[j] = r < 128 ? (at < n0 ? src0 + at : T) : (at < n1 ? src1 + at : T);
+            for (int b = 0; b < BOXES; ++b) {
+                uint8_t* dst = seg + b * SEG_ROWS * 128;
+                const int col = (w.tc * BOXES + b) * 64;
+                if constexpr (kRow) {  // a plain box: the tensor's edge clips it
+                    if (lane == 0) tma_load_2d(dst, &maps.box, &ring.full[s], col, src_h);
+                } else if (src_h + SEG_ROWS <= p.group_T) {
+                    if (lane == 0) tma_load_5d(dst, &maps.box, &ring.full[s], col, 0, 0, 0, src_h);
+                } else if (4 * lane < SEG_ROWS) {
+                    int y[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = Order::row(4 * lane + j);
+                        y[j] = r < n_h ? src_h + r : p.group_T;
+                    }
+                    tma_gather4(dst + 4 * lane * 128, &maps.gather, &ring.full[s], col, y[0], y[1], y[2], y[3]);
                 }
-#pragma unroll
-                for (int b = 0; b < BOXES; ++b)
-                    tma_gather4(tiles + s * (BOXES * BOX_BYTES) + b * BOX_BYTES + s4 * 128, tmap, &ring.full[s],
-                                (w.tc * BOXES + b) * 64, y[0], y[1], y[2], y[3]);
             }
         }
     }
     if (lane == 0) drain_loads(ring.full, nullptr, STAGES, i);  // no load lands after this CTA exits
+}
+
+// Rows of stage s's segment h (compute warps).
+template <int STAGES, int STAGE_BYTES>
+__device__ __forceinline__ int group_seg_rows(const uint8_t* tiles, int s, int h) {
+    return reinterpret_cast<const GroupSmem<STAGES>*>(tiles + STAGES * STAGE_BYTES)->rows[s][h];
+}
+
+// Four words of eight consecutive rows of a column (row 2i in the low half of
+// word i), of which the first `rem` are the group's.
+__device__ __forceinline__ uint4 mask_rows8(uint4 v, int rem) {
+    auto m = [rem](int i) { return rem >= 2 * i + 2 ? 0xFFFFFFFFu : rem == 2 * i + 1 ? 0x0000FFFFu : 0u; };
+    return make_uint4(v.x & m(0), v.y & m(1), v.z & m(2), v.w & m(3));
 }
 
 // CTA-wide max over the compute warps' values; thread 0 writes the partial.
@@ -931,7 +976,7 @@ constexpr bool issue_bound_mode() {
 // quantizing pass re-reads the tiles (from L2).
 template <int FMT, int RND, int NH, bool AMAX_ONLY, int STAGES, bool FUSED = false, bool GROUPED = false>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
-    quant_row_kernel(const __grid_constant__ CUtensorMap tmap, const QuantParams p) {
+    quant_row_kernel(const __grid_constant__ TileMap<GROUPED> tmap, const QuantParams p) {
     using Grp = Group<FMT, RND, NH>;
     constexpr int NB = Grp::NB;
     constexpr int G = AMAX_ONLY ? ((NH > 16) ? NH : 16) : Grp::G;
@@ -959,8 +1004,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
 
     if (warp == kComputeWarps) {
         if constexpr (GROUPED) {
-            gather_tiles<STAGES, kRowTileRows, 1, RowOrder>(&tmap, p.group_offsets, p.groups, p.group_T, ring, tiles,
-                                                           tiles_c, tiles_r, lane);
+            load_group_tiles<STAGES, 2, 128, 128, 1, STAGE_BYTES, RowOrder>(tmap, p, ring, tiles, tiles_c, tiles_r, lane);
             return;
         }
         // ---------------- producer ----------------
@@ -1036,16 +1080,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
         uint32_t codes[kRowTileCols / 8];
         uint32_t scodes[kRowTileCols / 16];
         uint32_t scw = 0;
-        // rows in groups: a warp whose rows are all no group's has zero codes and scales
-        bool nothing = false;
-        if constexpr (GROUPED)
-            nothing = ((warp & 3) << 5) >=
-                      reinterpret_cast<GroupSmem<STAGES>*>(tiles + STAGES * STAGE_BYTES)->rows[s][warp >> 2];
+        // rows in groups: this thread's row may be no group's (its codes and
+        // scales are zero), or the whole warp's
+        bool none = false, nothing = false;
+        const float amax_before = amax_acc;
+        if constexpr (GROUPED) {
+            const int n = group_seg_rows<STAGES, STAGE_BYTES>(tiles, s, warp >> 2);
+            none = (tid & 127) >= n;
+            nothing = ((warp & 3) << 5) >= n;
+        }
         if (nothing) {
-#pragma unroll
-            for (int i = 0; i < kRowTileCols / 8; ++i) codes[i] = 0;
-#pragma unroll
-            for (int i = 0; i < kRowTileCols / 16; ++i) scodes[i] = 0;
+            // nothing to read
         } else if constexpr (kPacked) {
             // chunk c of this thread's row: 16-byte chunk c ^ (tid % 8) of its 128-byte line
             const uint32_t rb = smem_u32(tiles) + (uint32_t)(s * STAGE_BYTES) + (uint32_t)tid * 128u +
@@ -1086,6 +1131,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
                               codes + g * (G / 8), scodes + g * (G / NB));
             }
         }
+        }
+        if constexpr (GROUPED) {
+            if (none) {
+                amax_acc = amax_before;
+                scw = 0;
+#pragma unroll
+                for (int i = 0; i < kRowTileCols / 8; ++i) codes[i] = 0;
+#pragma unroll
+                for (int i = 0; i < kRowTileCols / 16; ++i) scodes[i] = 0;
+            }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ring.empty[s]);
@@ -1144,7 +1199,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
 // x-rows Gq + 8u + [0, 8) of column c.
 template <int FMT, int RND, int NH, bool AMAX_ONLY, int STAGES, bool DUAL = false, bool GROUPED = false>
 __global__ void __launch_bounds__(kThreads, 2)
-    quant_col_kernel(const __grid_constant__ CUtensorMap tmap, const QuantParams p) {
+    quant_col_kernel(const __grid_constant__ TileMap<GROUPED> tmap, const QuantParams p) {
     using Grp = Group<FMT, RND, NH>;
     constexpr int NB = Grp::NB;
     constexpr int G = AMAX_ONLY ? ((NH > 16) ? NH : 16) : Grp::G;
@@ -1170,8 +1225,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     if (warp == kComputeWarps) {
         if constexpr (GROUPED) {
-            gather_tiles<STAGES, TILE_ROWS, 2, ColOrder<G>>(&tmap, p.group_offsets, p.groups, p.group_T, ring, tiles,
-                                                           tiles_c, tiles_r, lane);
+            load_group_tiles<STAGES, 1, TILE_ROWS, TILE_ROWS, 2, STAGE_BYTES, ColOrder<G>>(tmap, p, ring, tiles, tiles_c, tiles_r, lane);
             return;
         }
         if (lane == 0) {
@@ -1244,6 +1298,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int64_t c0 = (int64_t)w.tc * kColTileCols;
         const int64_t r0 = (int64_t)w.tr * TILE_ROWS;
         const uint32_t stage_base = smem_u32(tiles) + (uint32_t)(s * STAGE_BYTES);
+        int valid = G;  // rows in groups: of this thread's G rows, those that are the group's
+        if constexpr (GROUPED) valid = group_seg_rows<STAGES, STAGE_BYTES>(tiles, s, 0) - G * q;
         if constexpr (kSharedQuads) {
             if (shared_quads && quad_half == 0) {
                 int qtr = w.tr, qtc = w.tc;
@@ -1271,6 +1327,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                 asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                              : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
                              : "r"(addr));
+                if constexpr (GROUPED) {
+                    if (valid < G) {
+                        const uint4 m = mask_rows8(make_uint4(a0, a1, a2, a3), valid - 8 * u);
+                        a0 = m.x; a1 = m.y; a2 = m.z; a3 = m.w;
+                    }
+                }
                 if (NH > 0 && p.signs != 0u) {
                     a0 ^= smask[4 * u + 0];
                     a1 ^= smask[4 * u + 1];
@@ -1393,19 +1455,36 @@ __global__ void __launch_bounds__(kThreads, 2)
 // v = 4 n + l / 8; the 8 rows of a phase have s % 8 = l % 8 all distinct
 // (conflict-free with the 128-byte swizzle), and after the transposing load
 // lane (c, q) holds x-rows 64 q + 8 n + [0, 8) of column c in order.
+// A stage of the band kernels: the tile, with groups two segments kBandSegPitch
+// rows apart, rounded up to the swizzle pattern's 1024 bytes.
+template <bool GROUPED>
+constexpr int kBandStageBytes = GROUPED ? (2 * kBandSegPitch * 128 + 1023) / 1024 * 1024 : 256 * 128;
+// Address within a stage that lane gives its warp's first transposing load
+// (columns 8 warp .. + 7): row k + 2 q + 8 v of the tile, or of segment q / 2
+// (BandOrder: row k + 2 (q % 2) + 4 v); the 8 rows of a phase are all
+// different modulo 8 in both.
+template <bool GROUPED>
+__device__ __forceinline__ uint32_t band_lm_base(int warp, int lane) {
+    const int i = lane >> 3, q = (lane >> 1) & 3, k = lane & 1;  // matrix i: v = 4 n + i
+    const int row = GROUPED ? kBandSegPitch * (q >> 1) + k + 2 * (q & 1) + 4 * i : lane;
+    return (uint32_t)row * 128u + ((uint32_t)(warp ^ (row & 7)) << 4);
+}
 // Dual mode's row work on one band tile (see below): thread t quantizes
 // shared-memory row t of the stage at `stage`, x-row r = r0 + k + 2 v + 64 q
 // (t = k + 2 q + 8 v) over the tile's 64 columns, and stores its codes and
 // scale word(s) in the row orientation (rows = R, k = C).
-template <int FMT, int RND, int NH_ROW>
+template <int FMT, int RND, int NH_ROW, bool GROUPED>
 __device__ __forceinline__ void dual_row_work(const QuantParams& p, float s_enc_row, const float* rtab_row,
-                                              const float2* tab2_row, ScaleRng& srng, uint32_t stage, int tr, int tc) {
+                                              const float2* tab2_row, ScaleRng& srng, uint32_t stage, int tr, int tc, int seg_rows) {
     using GrpR = Group<FMT, RND, NH_ROW>;
     constexpr int NB = GrpR::NB;
     constexpr int GR = GrpR::G;
     constexpr bool kPackedRow = FMT == kNvfp4 && (NH_ROW == 0 || NH_ROW == 16) && RND != kSr;
-    const int t = threadIdx.x;
-    const int64_t r = (int64_t)tr * 256 + (t & 1) + 2 * (t >> 3) + 64 * ((t >> 1) & 3);
+    // shared-memory row t, and the x-row of the tile that it holds
+    const int t = GROUPED ? (int)threadIdx.x + (kBandSegPitch - 128) * (int)(threadIdx.x >> 7) : (int)threadIdx.x;
+    const int tile_row = GROUPED ? BandOrder::row(threadIdx.x & 127) + 128 * (int)(threadIdx.x >> 7)
+                                 : (t & 1) + 2 * (t >> 3) + 64 * ((t >> 1) & 3);
+    const int64_t r = (int64_t)tr * 256 + tile_row;
     const int64_t c0 = (int64_t)tc * 64;
     if (c0 >= p.C) return;  // the column tiles past C exist for the column orientation's padding only
     const uint32_t rbase = stage + (uint32_t)t * 128u;
@@ -1448,6 +1527,13 @@ __device__ __forceinline__ void dual_row_work(const QuantParams& p, float s_enc_
                        scodes + g * (GR / NB));
     }
     }
+    if (GROUPED && (tile_row & 127) >= seg_rows) {  // no group's row
+        scw = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) codes[i] = 0;
+#pragma unroll
+        for (int i = 0; i < 64 / NB; ++i) scodes[i] = 0;
+    }
     if (r < p.R) {
         uint8_t* dst = p.codes_row + r * (p.C / 2) + c0 / 2;
         if (c0 + 64 <= p.C) {
@@ -1487,13 +1573,16 @@ __device__ __forceinline__ void dual_row_work(const QuantParams& p, float s_enc_
 // would: one read of x gives both orientations.
 template <int FMT, int RND, int NH, int STAGES, int NH_ROW = -1, bool FUSED = false, bool GROUPED = false>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
-    quant_col64_kernel(const __grid_constant__ CUtensorMap tmap, const QuantParams p) {
+    quant_col64_kernel(const __grid_constant__ TileMap<GROUPED> tmap, const QuantParams p) {
     constexpr bool kDual = NH_ROW >= 0;
     using Grp = Group<FMT, RND, NH>;
     constexpr int NB = Grp::NB;
     constexpr int G = Grp::G;
     constexpr int TILE_ROWS = 256, TILE_COLS = 64;
-    constexpr int STAGE_BYTES = TILE_ROWS * TILE_COLS * 2;  // 32 KiB
+    constexpr int STAGE_BYTES = kBandStageBytes<GROUPED>;
+    constexpr uint32_t kTileBytes = TILE_ROWS * TILE_COLS * 2;  // 32 KiB
+    // shared-memory bytes between the transposing loads of a band
+    constexpr uint32_t kLmStep = GROUPED ? 2048 : 4096;
     static_assert(64 % G == 0, "groups tile a 64-row band");
     // NVFP4 with no Hadamard or a 16-point one, round-to-nearest or Quartet
     // II: the packed 64-element unit
@@ -1521,8 +1610,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
 
     if (warp == kComputeWarps) {
         if constexpr (GROUPED) {
-            gather_tiles<STAGES, TILE_ROWS, 1, BandOrder>(&tmap, p.group_offsets, p.groups, p.group_T, ring, tiles,
-                                                           tiles_c, tiles_r, lane);
+            load_group_tiles<STAGES, 2, 128, kBandSegPitch, 1, STAGE_BYTES, BandOrder>(tmap, p, ring, tiles, tiles_c, tiles_r, lane);
             return;
         }
         if (lane == 0) {
@@ -1535,7 +1623,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&ring.full[s], STAGE_BYTES);
+                    mbar_arrive_expect_tx(&ring.full[s], kTileBytes);
                     tma_load_4d(tiles + s * STAGE_BYTES, &tmap, &ring.full[s], w.tc * TILE_COLS, 0, 4 * w.tr, 0);
                 }
             drain_loads(ring.full, nullptr, STAGES, i);  // no load lands after this CTA exits
@@ -1583,7 +1671,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
     const int q = lane & 3;
     const int cc = warp * 8 + (lane >> 2);  // column within the tile
     // ldmatrix address of instruction n: lm_base + 4096 n (smem row lane + 32 n)
-    const uint32_t lm_base = (uint32_t)lane * 128u + ((uint32_t)(warp ^ (lane & 7)) << 4);
+    const uint32_t lm_base = band_lm_base<GROUPED>(warp, lane);
     const int64_t atom_row_bytes = (p.kb4 / 4) * 512;
     // sign masks held in registers, except in dual mode (registers for the row work)
     uint32_t smask[kDual || kPacked ? 1 : G / 2];
@@ -1599,6 +1687,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
         const int64_t c = (int64_t)w.tc * TILE_COLS + cc;          // x column = output row
         const int64_t rb = (int64_t)w.tr * TILE_ROWS + 64 * q;     // first k index of this thread's band
         const uint32_t stage_base = smem_u32(tiles) + (uint32_t)(s * STAGE_BYTES) + lm_base;
+        int valid = 64;  // rows in groups: of this thread's band, those that are the group's
+        if constexpr (GROUPED) valid = group_seg_rows<STAGES, STAGE_BYTES>(tiles, s, q >> 1) - 64 * (q & 1);
         uint32_t codes[8];
         uint32_t scodes[64 / NB];
         uint32_t scw = 0;
@@ -1608,7 +1698,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
                 uint4 v;
                 asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                              : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                             : "r"(stage_base + (uint32_t)(n * 4096)));
+                             : "r"(stage_base + (uint32_t)n * kLmStep));
+                if constexpr (GROUPED)
+                    if (valid < 64) v = mask_rows8(v, valid - 8 * n);
                 return v;
             };
             scw = nv64_quantize<RND, NH>(load, sf, s_enc, tab2, col_stream(p), (uint64_t)c * (uint64_t)p.k + (uint64_t)rb,
@@ -1619,11 +1711,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
             float v[G];
 #pragma unroll
             for (int u = 0; u < G / 8; ++u) {
-                const uint32_t addr = stage_base + (uint32_t)((g * (G / 8) + u) * 4096);
+                const uint32_t addr = stage_base + (uint32_t)(g * (G / 8) + u) * kLmStep;
                 uint32_t a0, a1, a2, a3;
                 asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                              : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
                              : "r"(addr));
+                if constexpr (GROUPED) {
+                    if (valid < 64) {
+                        const uint4 m = mask_rows8(make_uint4(a0, a1, a2, a3), valid - 8 * (g * (G / 8) + u));
+                        a0 = m.x; a1 = m.y; a2 = m.z; a3 = m.w;
+                    }
+                }
                 if (NH > 0 && p.signs != 0u) {
                     if constexpr (kDual) {
                         a0 ^= Grp::sign_mask(p.signs, 4 * u + 0);
@@ -1649,8 +1747,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
                           scodes + g * (G / NB));
         }
         }
-        if constexpr (kDual) dual_row_work<FMT, RND, NH_ROW>(p, s_enc_row, rtab_row, tab2_row, srng_row,
-                                                          smem_u32(tiles) + (uint32_t)(s * STAGE_BYTES), w.tr, w.tc);
+        if constexpr (kDual)
+            dual_row_work<FMT, RND, NH_ROW, GROUPED>(
+                p, s_enc_row, rtab_row, tab2_row, srng_row, smem_u32(tiles) + (uint32_t)(s * STAGE_BYTES), w.tr, w.tc,
+                GROUPED ? group_seg_rows<STAGES, STAGE_BYTES>(tiles, s, warp >> 2) : 128);
         __syncwarp();
         if (lane == 0) mbar_arrive(&ring.empty[s]);
         if (rb < p.k) {  // k is a multiple of 64: a band is wholly inside or wholly outside
@@ -1697,10 +1797,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
 
 template <int NH, int STAGES, bool GROUPED = false>
 __global__ void __launch_bounds__(kThreads, 2)
-    amax_rowcol64_kernel(const __grid_constant__ CUtensorMap tmap, const QuantParams p) {
+    amax_rowcol64_kernel(const __grid_constant__ TileMap<GROUPED> tmap, const QuantParams p) {
     static_assert(NH == 0 || NH == 16, "16-element groups");
     constexpr int TILE_ROWS = 256, TILE_COLS = 64;
-    constexpr int STAGE_BYTES = TILE_ROWS * TILE_COLS * 2;  // 32 KiB
+    constexpr int STAGE_BYTES = kBandStageBytes<GROUPED>;
+    constexpr uint32_t kTileBytes = TILE_ROWS * TILE_COLS * 2;  // 32 KiB
+    constexpr uint32_t kLmStep = GROUPED ? 2048 : 4096;
     extern __shared__ __align__(1024) uint8_t dyn_smem[];
     uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
     __shared__ Ring<STAGES> ring;
@@ -1718,8 +1820,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     pdl_launch_dependents();
     if (warp == kComputeWarps) {
         if constexpr (GROUPED) {
-            gather_tiles<STAGES, TILE_ROWS, 1, BandOrder>(&tmap, p.group_offsets, p.groups, p.group_T, ring, tiles,
-                                                           tiles_c, tiles_r, lane);
+            load_group_tiles<STAGES, 2, 128, kBandSegPitch, 1, STAGE_BYTES, BandOrder>(tmap, p, ring, tiles, tiles_c, tiles_r, lane);
             return;
         }
         if (lane == 0) {
@@ -1727,7 +1828,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (TileWalk<STAGES> w(tiles_c); w.tr < tiles_r; w.next(), ++i) {
                 const int s = w.stage;
                 if (i >= STAGES && !mbar_wait(&ring.empty[s], w.phase ^ 1u)) break;
-                mbar_arrive_expect_tx(&ring.full[s], STAGE_BYTES);
+                mbar_arrive_expect_tx(&ring.full[s], kTileBytes);
                 tma_load_4d(tiles + s * STAGE_BYTES, &tmap, &ring.full[s], w.tc * TILE_COLS, 0, 4 * w.tr, 0);
             }
             drain_loads(ring.full, nullptr, STAGES, i);  // no load lands after this CTA exits
@@ -1736,23 +1837,32 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     const SignFlips sf_col(NH > 0 ? p.signs : 0u), sf_row(NH > 0 ? p.signs_row : 0u);
     // ldmatrix address of instruction n: lm_base + 4096 n (smem row lane + 32 n)
-    const uint32_t lm_base = (uint32_t)lane * 128u + ((uint32_t)(warp ^ (lane & 7)) << 4);
-    const uint32_t row_off = (uint32_t)tid * 128u + ((uint32_t)(tid & 7) << 4);
+    const uint32_t lm_base = band_lm_base<GROUPED>(warp, lane);
+    const int srow = GROUPED ? tid + (kBandSegPitch - 128) * (tid >> 7) : tid;  // shared-memory row of the row work
+    const uint32_t row_off = (uint32_t)srow * 128u + ((uint32_t)(srow & 7) << 4);
     float m_col = 0.0f, m_row = 0.0f;
     for (TileWalk<STAGES> w(tiles_c); w.tr < tiles_r; w.next()) {
         const int s = w.stage;
         if (!mbar_wait(&ring.full[s], w.phase)) break;
         const uint32_t stage = smem_u32(tiles) + (uint32_t)(s * STAGE_BYTES);
+        int valid = 64;  // rows in groups: of this thread's band, those that are the group's
+        bool none = false;  // and whether its row is
+        if constexpr (GROUPED) {
+            valid = group_seg_rows<STAGES, STAGE_BYTES>(tiles, s, (lane & 3) >> 1) - 64 * (lane & 1);
+            none = BandOrder::row(tid & 127) >= group_seg_rows<STAGES, STAGE_BYTES>(tiles, s, warp >> 2);
+        }
         auto load_col = [&](int n) {
             uint4 v;
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                         : "r"(stage + lm_base + (uint32_t)(n * 4096)));
+                         : "r"(stage + lm_base + (uint32_t)n * kLmStep));
+            if constexpr (GROUPED)
+                if (valid < 64) v = mask_rows8(v, valid - 8 * n);
             return v;
         };
         m_col = rot_amax64<NH>(load_col, sf_col, m_col);
         auto load_row = [&](int c) { return lds128((stage + row_off) ^ ((uint32_t)c << 4)); };
-        m_row = rot_amax64<NH>(load_row, sf_row, m_row);
+        if (!none) m_row = rot_amax64<NH>(load_row, sf_row, m_row);
         __syncwarp();
         if (lane == 0) mbar_arrive(&ring.empty[s]);
     }
@@ -1778,9 +1888,15 @@ template <int STAGES>
 int ring_smem(int stage_bytes, const QuantParams& p) {
     return STAGES * stage_bytes + 1024 + (p.group_offsets != nullptr ? (int)sizeof(GroupSmem<STAGES>) : 0);
 }
+int band_stage_bytes(const QuantParams& p) {
+    return p.group_offsets != nullptr ? kBandStageBytes<true> : kBandStageBytes<false>;
+}
 
-template <typename Kern>
-cudaError_t launch_persistent(Kern kern, int grid, int smem, const CUtensorMap& tmap, const QuantParams& p,
+// The two maps of rows in groups (box, gather), one after the other.
+const GroupMaps& group_maps(const CUtensorMap* tmap) { return *reinterpret_cast<const GroupMaps*>(tmap); }
+
+template <typename Kern, typename Map>
+cudaError_t launch_persistent(Kern kern, int grid, int smem, const Map& tmap, const QuantParams& p,
                               cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -1826,7 +1942,8 @@ cudaError_t launch_t(const QuantParams& p, int axis, const CUtensorMap* tmap, in
         if (grid <= 0) grid = persistent_grid(tiles, kCtasPerSm<S>);
         const int smem = ring_smem<S>(kRowTileRows * kRowTileCols * 2, p);
         if (p.group_offsets != nullptr)
-            return launch_persistent(quant_row_kernel<FMT, RND, NH, AMAX_ONLY, S, false, true>, grid, smem, *tmap, p, s);
+            return launch_persistent(quant_row_kernel<FMT, RND, NH, AMAX_ONLY, S, false, true>, grid, smem,
+                                     group_maps(tmap), p, s);
         return launch_persistent(quant_row_kernel<FMT, RND, NH, AMAX_ONLY, S>, grid, smem, *tmap, p, s);
     } else {
         constexpr int NB = (FMT == kNvfp4) ? 16 : 32;
@@ -1838,8 +1955,8 @@ cudaError_t launch_t(const QuantParams& p, int axis, const CUtensorMap* tmap, in
         // rows in groups come here for the amax alone (they are quantized over bands)
         if constexpr (AMAX_ONLY)
             if (p.group_offsets != nullptr)
-                return launch_persistent(quant_col_kernel<FMT, RND, NH, AMAX_ONLY, S, false, true>, grid, smem, *tmap, p,
-                                         s);
+                return launch_persistent(quant_col_kernel<FMT, RND, NH, AMAX_ONLY, S, false, true>, grid, smem,
+                                         group_maps(tmap), p, s);
         return launch_persistent(quant_col_kernel<FMT, RND, NH, AMAX_ONLY, S>, grid, smem, *tmap, p, s);
     }
 }
@@ -1849,10 +1966,10 @@ template <int FMT, int RND, int NH>
 cudaError_t launch_col64(const QuantParams& p, const CUtensorMap* tmap, cudaStream_t s) {
     constexpr int S = issue_bound_mode<FMT, RND>() ? 2 : 3;
     const int64_t tiles = ((p.rows + 127) / 128 * 2) * ((p.k + 255) / 256);
-    const int smem = ring_smem<S>(256 * 64 * 2, p);
+    const int smem = ring_smem<S>(band_stage_bytes(p), p);
     if (p.group_offsets != nullptr)
         return launch_persistent(quant_col64_kernel<FMT, RND, NH, S, -1, false, true>,
-                                 persistent_grid(tiles, kCtasPerSm<S>), smem, *tmap, p, s);
+                                 persistent_grid(tiles, kCtasPerSm<S>), smem, group_maps(tmap), p, s);
     return launch_persistent(quant_col64_kernel<FMT, RND, NH, S>, persistent_grid(tiles, kCtasPerSm<S>), smem,
                              *tmap, p, s);
 }
@@ -1946,12 +2063,12 @@ template <int FMT, int RND, int NH, int NH_ROW>
 cudaError_t launch_dual_t(const QuantParams& p, const CUtensorMap* tmap, cudaStream_t s) {
     constexpr int S = 3;
     const int64_t tiles = ((p.rows + 127) / 128 * 2) * ((p.k + 255) / 256);
-    const int smem = ring_smem<S>(256 * 64 * 2, p);
+    const int smem = ring_smem<S>(band_stage_bytes(p), p);
     // rows in groups come here to be rounded to nearest alone (the linear layer's one read of dY)
     if constexpr (RND == kRtn)
         if (p.group_offsets != nullptr)
             return launch_persistent(quant_col64_kernel<FMT, RND, NH, S, NH_ROW, false, true>, persistent_grid(tiles, 2),
-                                     smem, *tmap, p, s);
+                                     smem, group_maps(tmap), p, s);
     return launch_persistent(quant_col64_kernel<FMT, RND, NH, S, NH_ROW>, persistent_grid(tiles, 2), smem, *tmap, p,
                              s);
 }
@@ -1978,10 +2095,10 @@ cudaError_t launch_quant_dual(const QuantParams& p, int fmt, int rnd, int nh, in
 cudaError_t launch_amax_rowcol64(const QuantParams& p, int nh, const CUtensorMap* tmap, int n_partials,
                                  cudaStream_t s) {
     constexpr int S = 3;
-    const int smem = ring_smem<S>(256 * 64 * 2, p);
+    const int smem = ring_smem<S>(band_stage_bytes(p), p);
     if (p.group_offsets != nullptr)
-        return nh == 16 ? launch_persistent(amax_rowcol64_kernel<16, S, true>, n_partials, smem, *tmap, p, s)
-                        : launch_persistent(amax_rowcol64_kernel<0, S, true>, n_partials, smem, *tmap, p, s);
+        return nh == 16 ? launch_persistent(amax_rowcol64_kernel<16, S, true>, n_partials, smem, group_maps(tmap), p, s)
+                        : launch_persistent(amax_rowcol64_kernel<0, S, true>, n_partials, smem, group_maps(tmap), p, s);
     if (nh == 16) return launch_persistent(amax_rowcol64_kernel<16, S>, n_partials, smem, *tmap, p, s);
     return launch_persistent(amax_rowcol64_kernel<0, S>, n_partials, smem, *tmap, p, s);
 }
