@@ -833,7 +833,8 @@ int amax_rowcol_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t ha
     float* partials = static_cast<float*>(workspace);
     const int nh = had_n(had_col);
     cudaError_t e;
-    if (nh <= 16 && had_n(had_row) == nh) {
+    // (rows in groups: sizes of 0 and 16 may differ)
+    if (nh <= 16 && (gr != nullptr ? had_n(had_row) <= 16 : had_n(had_row) == nh)) {
         QuantParams p{};
         set_groups(p, gr);
         p.x = static_cast<const uint16_t*>(x);
@@ -853,7 +854,7 @@ int amax_rowcol_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t ha
         if (bands) {
             if ((rc = gr ? make_group_tmaps(tm, x, gr->T, C, ld, QFP4_AXIS_COL, 0) : make_col64_tmap(tm, x, R, C, ld)))
                 return rc;
-            e = launch_amax_rowcol64(p, nh, tm, n, s);
+            e = launch_amax_rowcol64(p, nh, had_n(had_row), tm, n, s);
         } else {
             if ((rc = make_input_tmap(tm, x, R, C, ld, QFP4_AXIS_COL, 16))) return rc;
             e = launch_amax_rowcol(p, nh, tm, n, s);
@@ -1059,12 +1060,13 @@ int linear_fwd_impl(const void* X, const void* W, void* Y, int64_t M, int64_t N,
 
 // dY (M x N, contiguous) quantized along N for Dgrad into out_row, and for
 // Wgrad along M into out_col where one read gives both: then *col_done is set,
-// else *am_col is what the column quantization takes. When both are NVFP4 with the same
-// Hadamard (size <= 16; the sign vectors differ per GEMM), one read of dY gives
-// both tensor amaxes. When both quantizations round to nearest with the same
-// format, one more read gives both quantized operands (memory-bound, so one
-// read instead of two is a quarter faster); stochastic and Quartet II rounding
-// are bound by instruction issue, and there the two separate passes are faster.
+// else *am_col is what the column quantization takes. When both are NVFP4 with
+// the same Hadamard (size <= 16; the sign vectors differ per GEMM; with rows in
+// groups any two such sizes), one read of dY gives both tensor amaxes. When
+// both quantizations round to nearest with the same format, one more read gives
+// both quantized operands (memory-bound, so one read instead of two is a
+// quarter faster); stochastic and Quartet II rounding are bound by instruction
+// issue, and there the two separate passes are faster.
 // dy_amax: two floats; partials: the quantizers' workspace.
 int quantize_dy(const void* dY, int64_t M, int64_t N, const qfp4_recipe* recipe, const qfp4_seed* seed,
                 qfp4_tensor* out_row, qfp4_tensor* out_col, float* dy_amax, float* partials, bool* col_done,
@@ -1079,8 +1081,9 @@ int quantize_dy(const void* dY, int64_t M, int64_t N, const qfp4_recipe* recipe,
     *am_col = nullptr;
     *col_done = dual;
     int rc;
-    if (d.fmt == QFP4_NVFP4 && w.fmt == QFP4_NVFP4 && d.had == w.had && had_n(d.had) <= 16) {
-        if ((rc = amax_rowcol_impl(dY, M, N, N, d.had, d.had, &s0, &s2, dy_amax, dy_amax + 1, partials, pws, s,
+    if (d.fmt == QFP4_NVFP4 && w.fmt == QFP4_NVFP4 &&
+        (gr != nullptr ? had_n(d.had) <= 16 && had_n(w.had) <= 16 : d.had == w.had && had_n(d.had) <= 16)) {
+        if ((rc = amax_rowcol_impl(dY, M, N, N, d.had, w.had, &s0, &s2, dy_amax, dy_amax + 1, partials, pws, s,
                                    gr)))
             return rc;
         am_row = dy_amax;

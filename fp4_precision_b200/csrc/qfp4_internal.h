@@ -87,8 +87,9 @@ cudaError_t launch_quant_dual(const QuantParams& p, int fmt, int rnd, int nh, in
 // to p.amax_out_row (n_partials each). nh: 0 or 16.
 cudaError_t launch_amax_rowcol(const QuantParams& p, int nh, const CUtensorMap* tmap, int n_partials, cudaStream_t s);
 // The same over 64-row bands (R a multiple of 64; tmap: the 4-D band view),
-// both orientations as two packed pairs of 16-element groups per thread.
-cudaError_t launch_amax_rowcol64(const QuantParams& p, int nh, const CUtensorMap* tmap, int n_partials,
+// both orientations as two packed pairs of 16-element groups per thread. nh_row:
+// the row orientation's size, nh's but for rows in groups.
+cudaError_t launch_amax_rowcol64(const QuantParams& p, int nh, int nh_row, const CUtensorMap* tmap, int n_partials,
                                  cudaStream_t s);
 // Tiles the band amax pass walks (rows, k of the column orientation).
 int64_t amax_rowcol64_tiles(int64_t rows, int64_t k);

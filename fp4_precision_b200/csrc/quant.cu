@@ -1795,10 +1795,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
 // 1/sqrt(n_h) is applied once to each CTA's maxima (rounding c * y is
 // monotone in y). Zero-filled columns and rows past the tensor add nothing.
 
-template <int NH, int STAGES, bool GROUPED = false>
+template <int NH, int STAGES, bool GROUPED = false, int NH_ROW = NH>
 __global__ void __launch_bounds__(kThreads, 2)
     amax_rowcol64_kernel(const __grid_constant__ TileMap<GROUPED> tmap, const QuantParams p) {
-    static_assert(NH == 0 || NH == 16, "16-element groups");
+    static_assert((NH == 0 || NH == 16) && (NH_ROW == 0 || NH_ROW == 16), "16-element groups");
     constexpr int TILE_ROWS = 256, TILE_COLS = 64;
     constexpr int STAGE_BYTES = kBandStageBytes<GROUPED>;
     constexpr uint32_t kTileBytes = TILE_ROWS * TILE_COLS * 2;  // 32 KiB
@@ -1835,7 +1835,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         return;
     }
-    const SignFlips sf_col(NH > 0 ? p.signs : 0u), sf_row(NH > 0 ? p.signs_row : 0u);
+    const SignFlips sf_col(NH > 0 ? p.signs : 0u), sf_row(NH_ROW > 0 ? p.signs_row : 0u);
     // ldmatrix address of instruction n: lm_base + 4096 n (smem row lane + 32 n)
     const uint32_t lm_base = band_lm_base<GROUPED>(warp, lane);
     const int srow = GROUPED ? tid + (kBandSegPitch - 128) * (tid >> 7) : tid;  // shared-memory row of the row work
@@ -1862,14 +1862,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         };
         m_col = rot_amax64<NH>(load_col, sf_col, m_col);
         auto load_row = [&](int c) { return lds128((stage + row_off) ^ ((uint32_t)c << 4)); };
-        if (!none) m_row = rot_amax64<NH>(load_row, sf_row, m_row);
+        if (!none) m_row = rot_amax64<NH_ROW>(load_row, sf_row, m_row);
         __syncwarp();
         if (lane == 0) mbar_arrive(&ring.empty[s]);
     }
-    if constexpr (NH > 0) {
-        m_col = __fmul_rn(m_col, had_norm<NH>());  // c * max |y| = max |c * y|
-        m_row = __fmul_rn(m_row, had_norm<NH>());
-    }
+    // c * max |y| = max |c * y|
+    if constexpr (NH > 0) m_col = __fmul_rn(m_col, had_norm<NH>());
+    if constexpr (NH_ROW > 0) m_row = __fmul_rn(m_row, had_norm<NH_ROW>());
     write_partial(m_col, red, p.amax_out);
     write_partial(m_row, red + 16, p.amax_out_row);
 }
@@ -2092,13 +2091,16 @@ cudaError_t launch_quant_dual(const QuantParams& p, int fmt, int rnd, int nh, in
     return dispatch_dual<kMxfp4, kQuartet2>(p, nh, nh_row, tmap, s);
 }
 
-cudaError_t launch_amax_rowcol64(const QuantParams& p, int nh, const CUtensorMap* tmap, int n_partials,
+cudaError_t launch_amax_rowcol64(const QuantParams& p, int nh, int nh_row, const CUtensorMap* tmap, int n_partials,
                                  cudaStream_t s) {
     constexpr int S = 3;
     const int smem = ring_smem<S>(band_stage_bytes(p), p);
-    if (p.group_offsets != nullptr)
-        return nh == 16 ? launch_persistent(amax_rowcol64_kernel<16, S, true>, n_partials, smem, group_maps(tmap), p, s)
-                        : launch_persistent(amax_rowcol64_kernel<0, S, true>, n_partials, smem, group_maps(tmap), p, s);
+    if (p.group_offsets != nullptr) {
+        auto run = [&](auto* kern) { return launch_persistent(kern, n_partials, smem, group_maps(tmap), p, s); };
+        if (nh == 16)
+            return nh_row == 16 ? run(amax_rowcol64_kernel<16, S, true, 16>) : run(amax_rowcol64_kernel<16, S, true, 0>);
+        return nh_row == 16 ? run(amax_rowcol64_kernel<0, S, true, 16>) : run(amax_rowcol64_kernel<0, S, true, 0>);
+    }
     if (nh == 16) return launch_persistent(amax_rowcol64_kernel<16, S>, n_partials, smem, *tmap, p, s);
     return launch_persistent(amax_rowcol64_kernel<0, S>, n_partials, smem, *tmap, p, s);
 }

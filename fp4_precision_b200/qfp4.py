@@ -8,6 +8,7 @@ not a B200 the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -397,92 +398,148 @@ def linear_bwd(dY, X, W, rec: Recipe, seed: Seed, dX=None, dW=None, workspace=No
 
 
 # ---------------------------------------------------------------------------
+# The calls below run on the stream that is current on their tensors' device,
+# whichever device is current, or on the one given; what they allocate belongs
+# to that stream too.
+
+_WS_FLOATS = 1024  # the quantizers' workspace as fp32 words
+
+
+def _on_stream(f):
+    @functools.wraps(f)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return f(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return f(*args, **kwargs)
+    return call
+
+
+def _go(fn, what: str, i: int, *args):
+    h = torch._C._cuda_getCurrentRawStream(i)
+    if i == torch._C._cuda_getDevice():
+        status = fn(*args, h)
+    else:
+        with torch.cuda.device(i):
+            status = fn(*args, h)
+    if status != OK:
+        raise QFP4Error(status, what)
+
+
+def _gpu(t: torch.Tensor) -> int:
+    """Index of the GPU that t is on."""
+    i = t.get_device()
+    assert i >= 0, "tensors on a GPU"
+    return i
+
+
+def _matrix(t: torch.Tensor, shape, i: int, dtype=torch.bfloat16) -> int:
+    """Check a matrix with contiguous rows on GPU i; its row stride (a single row's is not looked at)."""
+    assert t.dtype is dtype and t.shape == shape and t.get_device() == i and (t.stride(1) == 1 or shape[1] <= 1)
+    return t.stride(0) if shape[0] > 1 else max(shape[1], 8)
+
+
+def _vector(t: torch.Tensor, n: int, dtype, i: int) -> int:
+    """Check a contiguous vector of n on GPU i; its address."""
+    assert t.dtype is dtype and t.shape == (n,) and (n <= 1 or t.stride(0) == 1) and t.get_device() == i
+    return t.data_ptr()
+
+
+def _ref(seed: Seed | None):
+    return None if seed is None else ctypes.byref(seed)
+
+
+def _workspace(given, nbytes: int, like: torch.Tensor):
+    """Address and size of a workspace, and the tensor that holds it."""
+    if given is None:
+        given = like.new_empty((nbytes,), dtype=torch.uint8)
+    return given.data_ptr(), given.numel() * given.element_size(), given
+
+
+# ---------------------------------------------------------------------------
 # RMSNorm
 
-def _matrix(t: torch.Tensor, like: torch.Tensor | None = None, dtype=torch.bfloat16) -> torch.Tensor:
-    """Check a 2-D tensor with contiguous rows (of `like`'s shape and device)."""
-    assert t.dtype == dtype and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1)
-    assert like is None or (t.shape == like.shape and t.device == like.device)
-    return t
+def _residual(x, res, h, shape, i: int):
+    """h (x itself without res and a buffer for it), its address and stride, and res's."""
+    if res is None and (h is None or h is x):
+        return x, None, 0, None, 0
+    h = torch.empty_like(x) if h is None else h
+    ldh = _matrix(h, shape, i)
+    return (h, h.data_ptr(), ldh, None, 0) if res is None else (h, h.data_ptr(), ldh, res.data_ptr(),
+                                                                _matrix(res, shape, i))
 
 
-def _ld(t: torch.Tensor | None) -> int:
-    """Row stride of a matrix (a single row's is not looked at)."""
-    if t is None:
-        return 0
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 8)
-
-
-def _norm_outputs(x, w, res, y, h, rstd, want_y=True):
-    R, C = _matrix(x).shape
-    assert w.dtype == torch.bfloat16 and w.shape == (C,) and w.is_contiguous() and w.device == x.device
-    assert res is None or _matrix(res, x) is res
-    if want_y:
-        y = torch.empty((R, C), dtype=torch.bfloat16, device=x.device) if y is None else _matrix(y, x)
-    if res is None:
-        h = x if h is None else _matrix(h, x)
-    else:
-        h = torch.empty((R, C), dtype=torch.bfloat16, device=x.device) if h is None else _matrix(h, x)
-    if rstd is None:
-        rstd = torch.empty((R,), dtype=torch.float32, device=x.device)
-    assert rstd.dtype == torch.float32 and rstd.shape == (R,) and rstd.is_contiguous() and rstd.device == x.device
-    return y, h, rstd
-
-
+@_on_stream
 def rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, eps: float, res: torch.Tensor | None = None, had: int = HAD_NONE,
                 seed: Seed | None = None, want_amax: bool = False, y=None, h=None, rstd=None, y_amax=None,
-                workspace=None, stream=None):
+                workspace=None):
     """h = x + res, y = h / rms(h) * w; see qfp4_rmsnorm_fwd. Returns (y, h,
     rstd, y_amax): without res, h is x itself unless a buffer for it is given;
     y_amax, y's NVFP4 tensor amax after the rotation `had`, is None unless
     wanted (want_amax or a buffer for it)."""
-    y, h, rstd = _norm_outputs(x, w, res, y, h, rstd)
-    if want_amax and y_amax is None:
-        y_amax = torch.empty((1,), dtype=torch.float32, device=x.device)
-    if y_amax is not None and workspace is None:
-        workspace = torch.empty((quantize_workspace_bytes(),), dtype=torch.uint8, device=x.device)
-    hp = None if res is None and h is x else h
-    _check(lib().qfp4_rmsnorm_fwd(_ptr(x), _ld(x), _ptr(res), _ld(res), _ptr(w), *x.shape, eps, _ptr(hp), _ld(hp),
-                                  _ptr(y), _ld(y), _ptr(rstd), had, None if seed is None else ctypes.byref(seed),
-                                  _ptr(y_amax), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                  _stream(stream)), "qfp4_rmsnorm_fwd")
+    shape, i = x.shape, _gpu(x)
+    ldx = _matrix(x, shape, i)
+    R, C = shape
+    y = torch.empty_like(x) if y is None else y
+    h, hp, ldh, rp, ldr = _residual(x, res, h, shape, i)
+    amax = want_amax or y_amax is not None
+    ap, wsp, wsb = None, None, 0
+    if amax and rstd is None and y_amax is None and workspace is None:
+        # one allocation for the three
+        workspace = x.new_empty((_WS_FLOATS + 4 + R,), dtype=torch.float32)
+        y_amax, rstd = workspace[_WS_FLOATS:_WS_FLOATS + 1], workspace[_WS_FLOATS + 4:]
+        wsp, wsb = workspace.data_ptr(), 4 * _WS_FLOATS
+        ap, rsp = wsp + 4 * _WS_FLOATS, wsp + 4 * (_WS_FLOATS + 4)
+    else:
+        rstd = x.new_empty((R,), dtype=torch.float32) if rstd is None else rstd
+        rsp = _vector(rstd, R, torch.float32, i)
+        if amax:
+            y_amax = x.new_empty((1,), dtype=torch.float32) if y_amax is None else y_amax
+            ap = _vector(y_amax, 1, torch.float32, i)
+            wsp, wsb, workspace = _workspace(workspace, 4 * _WS_FLOATS, x)
+    _go(lib().qfp4_rmsnorm_fwd, "qfp4_rmsnorm_fwd", i, x.data_ptr(), ldx, rp, ldr, _vector(w, C, torch.bfloat16, i), R,
+        C, eps, hp, ldh, y.data_ptr(), _matrix(y, shape, i), rsp, had, _ref(seed), ap, wsp, wsb)
     return y, h, rstd, y_amax
 
 
+@_on_stream
 def rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, eps: float, res: torch.Tensor | None = None, fmt: int = MXFP4,
                      had: int = HAD_NONE, seed: Seed | None = None, want_y: bool = True, y=None, h=None, rstd=None,
-                     out: QTensor | None = None, stream=None):
+                     out: QTensor | None = None):
     """rmsnorm_fwd and y's MXFP4 (or MXFP4_RU) quantization along its rows; see
     qfp4_rmsnorm_quantize. Returns (y, h, rstd, q); y is None unless wanted."""
-    y, h, rstd = _norm_outputs(x, w, res, y, h, rstd, want_y or y is not None)
-    out = empty_qtensor(MXFP4, x.shape[0], x.shape[1], x.device) if out is None else out
-    hp = None if res is None and h is x else h
-    _check(lib().qfp4_rmsnorm_quantize(_ptr(x), _ld(x), _ptr(res), _ld(res), _ptr(w), *x.shape, eps, _ptr(hp), _ld(hp),
-                                       _ptr(y), _ld(y), _ptr(rstd), fmt, had,
-                                       None if seed is None else ctypes.byref(seed), ctypes.byref(out.desc),
-                                       _stream(stream)), "qfp4_rmsnorm_quantize")
+    shape, i = x.shape, _gpu(x)
+    ldx = _matrix(x, shape, i)
+    R, C = shape
+    if y is None and want_y:
+        y = torch.empty_like(x)
+    h, hp, ldh, rp, ldr = _residual(x, res, h, shape, i)
+    rstd = x.new_empty((R,), dtype=torch.float32) if rstd is None else rstd
+    out = empty_qtensor(MXFP4, R, C, x.device) if out is None else out
+    _go(lib().qfp4_rmsnorm_quantize, "qfp4_rmsnorm_quantize", i, x.data_ptr(), ldx, rp, ldr,
+        _vector(w, C, torch.bfloat16, i), R, C, eps, hp, ldh, None if y is None else y.data_ptr(),
+        0 if y is None else _matrix(y, shape, i), _vector(rstd, R, torch.float32, i), fmt, had, _ref(seed),
+        ctypes.byref(out.desc))
     return y, h, rstd, out
 
 
+@_on_stream
 def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: torch.Tensor, dh: torch.Tensor | None = None,
-                dx=None, dw=None, accumulate: bool = False, workspace=None, stream=None):
+                dx=None, dw=None, accumulate: bool = False, workspace=None):
     """Gradients (dx, dw) of rmsnorm_fwd from y's gradient and (dh) h's own;
     see qfp4_rmsnorm_bwd. dx is the gradient of x and of res alike; dw is fp32."""
-    R, C = _matrix(dy).shape
-    _matrix(h, dy)
-    assert w.dtype == torch.bfloat16 and w.shape == (C,) and w.is_contiguous() and w.device == dy.device
-    assert rstd.dtype == torch.float32 and rstd.shape == (R,) and rstd.is_contiguous() and rstd.device == dy.device
-    assert dh is None or _matrix(dh, dy) is dh
-    dx = torch.empty((R, C), dtype=torch.bfloat16, device=dy.device) if dx is None else _matrix(dx, dy)
+    shape, i = dy.shape, _gpu(dy)
+    lddy = _matrix(dy, shape, i)
+    R, C = shape
+    dx = torch.empty_like(dy) if dx is None else dx
     if accumulate and dw is None:
         raise ValueError("accumulate adds into dw: pass the buffer")
-    dw = torch.empty((C,), dtype=torch.float32, device=dy.device) if dw is None else dw
-    assert dw.dtype == torch.float32 and dw.shape == (C,) and dw.is_contiguous() and dw.device == dy.device
-    if workspace is None:
-        workspace = torch.empty((lib().qfp4_rmsnorm_bwd_workspace_bytes(R, C),), dtype=torch.uint8, device=dy.device)
-    _check(lib().qfp4_rmsnorm_bwd(_ptr(dy), _ld(dy), _ptr(h), _ld(h), _ptr(w), _ptr(rstd), _ptr(dh), _ld(dh), R, C,
-                                  _ptr(dx), _ld(dx), _ptr(dw), 1 if accumulate else 0, _ptr(workspace),
-                                  workspace.numel(), _stream(stream)), "qfp4_rmsnorm_bwd")
+    dw = dy.new_empty((C,), dtype=torch.float32) if dw is None else dw
+    wsp, wsb, workspace = _workspace(workspace, lib().qfp4_rmsnorm_bwd_workspace_bytes(R, C), dy)
+    _go(lib().qfp4_rmsnorm_bwd, "qfp4_rmsnorm_bwd", i, dy.data_ptr(), lddy, h.data_ptr(), _matrix(h, shape, i),
+        _vector(w, C, torch.bfloat16, i), _vector(rstd, R, torch.float32, i), None if dh is None else dh.data_ptr(),
+        0 if dh is None else _matrix(dh, shape, i), R, C, dx.data_ptr(), _matrix(dx, shape, i),
+        _vector(dw, C, torch.float32, i), 1 if accumulate else 0, wsp, wsb)
     return dx, dw
 
 
@@ -494,60 +551,68 @@ def group_rows(T: int, E: int) -> int:
     return lib().qfp4_group_rows(T, E)
 
 
-def _groups(offsets: torch.Tensor, like: torch.Tensor) -> int:
-    """Check the group offsets (int32 [E + 1] on the tensors' device); E."""
-    assert offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.is_contiguous() and offsets.numel() >= 2
-    assert offsets.device == like.device
-    return offsets.numel() - 1
+def _groups(offsets: torch.Tensor, i: int) -> int:
+    """Check the group offsets (int32 [E + 1] on GPU i); E."""
+    n = offsets.shape[0]
+    assert n >= 2
+    _vector(offsets, n, torch.int32, i)
+    return n - 1
 
 
+@_on_stream
 def quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, fmt: int, rounding: int, had: int, axis: int,
                      seed: Seed | None = None, amax_in: torch.Tensor | None = None, out: QTensor | None = None,
-                     workspace=None, stream=None) -> QTensor:
+                     workspace=None) -> QTensor:
     """Quantize rows sorted by group, in the padded layout; see qfp4_quantize_grouped."""
-    T, C = _matrix(x).shape
-    E = _groups(offsets, x)
-    Tp = group_rows(T, E)
-    rows, k = (Tp, C) if axis == ROW else (C, Tp)
-    out = empty_qtensor(fmt, max(rows, 0), max(k, 0), x.device) if out is None else out
-    if workspace is None:
-        workspace = torch.empty((quantize_workspace_bytes(),), dtype=torch.uint8, device=x.device)
-    seed = seed or make_seed()
-    _check(lib().qfp4_quantize_grouped(_ptr(x), T, C, _ld(x), _ptr(offsets), E, fmt, rounding, had, axis,
-                                       ctypes.byref(seed), _ptr(amax_in), ctypes.byref(out.desc), _ptr(workspace),
-                                       workspace.numel(), _stream(stream)), "qfp4_quantize_grouped")
+    shape, i = x.shape, _gpu(x)
+    ldx = _matrix(x, shape, i)
+    T, C = shape
+    E = _groups(offsets, i)
+    if out is None:
+        Tp = max(group_rows(T, E), 0)
+        out = empty_qtensor(fmt, *((Tp, C) if axis == ROW else (C, Tp)), x.device)
+    wsp, wsb = None, 0
+    if amax_in is None and fmt == NVFP4:
+        wsp, wsb, workspace = _workspace(workspace, 4 * _WS_FLOATS, x)
+    _go(lib().qfp4_quantize_grouped, "qfp4_quantize_grouped", i, x.data_ptr(), T, C, ldx, offsets.data_ptr(), E, fmt,
+        rounding, had, axis, ctypes.byref(seed or make_seed()),
+        None if amax_in is None else _vector(amax_in, 1, torch.float32, i), ctypes.byref(out.desc), wsp, wsb)
     return out
 
 
+@_on_stream
 def gemm_grouped(A: QTensor, B: QTensor, offsets: torch.Tensor, T: int, out_dtype=torch.bfloat16,
-                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                 out: torch.Tensor | None = None) -> torch.Tensor:
     """Each group's rows of A times its part of B, as T rows; see
     qfp4_gemm_grouped. Rows of no group are not written."""
-    E = _groups(offsets, A.codes)
-    N = B.rows // E if B.k == A.k else B.rows
-    if out is None:
-        out = torch.empty((T, N), dtype=out_dtype, device=A.codes.device)
-    _matrix(out, dtype=out.dtype)
-    assert out.shape == (T, N) and out.dtype in (torch.bfloat16, torch.float32) and out.device == A.codes.device
-    dt = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
-    _check(lib().qfp4_gemm_grouped(ctypes.byref(A.desc), ctypes.byref(B.desc), _ptr(offsets), E, T, _ptr(out),
-                                   _ld(out), dt, _stream(stream)), "qfp4_gemm_grouped")
+    i = _gpu(A.codes)
+    E = _groups(offsets, i)
+    a, b = A.desc, B.desc
+    N = b.rows // E if b.k == a.k else b.rows
+    out = A.codes.new_empty((T, N), dtype=out_dtype) if out is None else out
+    f32 = out.dtype is torch.float32
+    ldd = _matrix(out, (T, N), i, torch.float32 if f32 else torch.bfloat16)
+    assert B.codes.get_device() == i
+    _go(lib().qfp4_gemm_grouped, "qfp4_gemm_grouped", i, ctypes.byref(a), ctypes.byref(b), offsets.data_ptr(), E, T,
+        out.data_ptr(), ldd, OUT_F32 if f32 else OUT_BF16)
     return out
 
 
+@_on_stream
 def gemm_grouped_wgrad(A: QTensor, B: QTensor, offsets: torch.Tensor, T: int, out_dtype=torch.float32,
-                       out: torch.Tensor | None = None, accumulate: bool = False, stream=None) -> torch.Tensor:
+                       out: torch.Tensor | None = None, accumulate: bool = False) -> torch.Tensor:
     """Per group, the product over its tokens [E, A.rows, B.rows]; see qfp4_gemm_grouped_wgrad."""
-    E = _groups(offsets, A.codes)
+    i = _gpu(A.codes)
+    E = _groups(offsets, i)
     if accumulate and out is None:
         raise ValueError("accumulate adds into out: pass the buffer")
     if out is None:
-        out = torch.empty((E, A.rows, B.rows), dtype=out_dtype, device=A.codes.device)
-    assert out.shape == (E, A.rows, B.rows) and out.is_contiguous() and out.device == A.codes.device
+        out = A.codes.new_empty((E, A.rows, B.rows), dtype=out_dtype)
+    assert out.shape == (E, A.rows, B.rows) and out.is_contiguous() and out.get_device() == i == B.codes.get_device()
     assert out.dtype in (torch.bfloat16, torch.float32)
-    dt = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
-    _check(lib().qfp4_gemm_grouped_wgrad(ctypes.byref(A.desc), ctypes.byref(B.desc), _ptr(offsets), E, T, _ptr(out), dt,
-                                         1 if accumulate else 0, _stream(stream)), "qfp4_gemm_grouped_wgrad")
+    _go(lib().qfp4_gemm_grouped_wgrad, "qfp4_gemm_grouped_wgrad", i, ctypes.byref(A.desc),
+        ctypes.byref(B.desc), offsets.data_ptr(), E, T, out.data_ptr(),
+        OUT_F32 if out.dtype == torch.float32 else OUT_BF16, 1 if accumulate else 0)
     return out
 
 
@@ -557,45 +622,47 @@ def linear_grouped_workspace_bytes(backward: bool, T: int, E: int, N: int, K: in
 
 def _linear_grouped_args(X, W, offsets):
     T, K = X.shape
-    E, N = W.shape[:2]
-    assert X.dtype == W.dtype == torch.bfloat16 and W.shape == (E, N, K) and X.device == W.device
-    assert X.is_contiguous() and W.is_contiguous() and _groups(offsets, X) == E
-    return T, E, N, K
+    E, N, _ = W.shape
+    i = _gpu(X)
+    assert X.dtype == W.dtype == torch.bfloat16 and W.shape[2] == K and i == W.get_device()
+    assert X.is_contiguous() and W.is_contiguous() and _groups(offsets, i) == E
+    return T, E, N, K, i
 
 
-def linear_grouped_fwd(X, W, offsets, rec: Recipe, seed: Seed, x_amax=None, Y=None, workspace=None,
-                       stream=None) -> torch.Tensor:
+def _linear_output(t, shape, code: int, like: torch.Tensor) -> torch.Tensor:
+    if t is None:
+        return like.new_empty(shape, dtype=_dtype(code))
+    assert t.shape == shape and t.dtype == _dtype(code) and t.is_contiguous() and t.get_device() == like.get_device()
+    return t
+
+
+@_on_stream
+def linear_grouped_fwd(X, W, offsets, rec: Recipe, seed: Seed, x_amax=None, Y=None, workspace=None) -> torch.Tensor:
     """Y[t] = X[t] W_e^T for the rows t of group e, W [E, N, K]; see
     qfp4_linear_grouped_fwd. Rows of Y that are no group's are not written."""
-    T, E, N, K = _linear_grouped_args(X, W, offsets)
-    Y = torch.empty((T, N), dtype=_dtype(rec.y_dtype), device=X.device) if Y is None else Y
-    assert Y.shape == (T, N) and Y.dtype == _dtype(rec.y_dtype) and Y.is_contiguous() and Y.device == X.device
-    if workspace is None:
-        workspace = torch.empty((linear_grouped_workspace_bytes(False, T, E, N, K, rec),), dtype=torch.uint8,
-                                device=X.device)
-    _check(lib().qfp4_linear_grouped_fwd(_ptr(X), _ptr(W), _ptr(Y), _ptr(offsets), E, T, N, K, ctypes.byref(rec),
-                                         ctypes.byref(seed), _ptr(x_amax), _ptr(workspace), workspace.numel(),
-                                         _stream(stream)), "qfp4_linear_grouped_fwd")
+    T, E, N, K, i = _linear_grouped_args(X, W, offsets)
+    Y = _linear_output(Y, (T, N), rec.y_dtype, X)
+    wsp, wsb, workspace = _workspace(workspace, linear_grouped_workspace_bytes(False, T, E, N, K, rec), X)
+    _go(lib().qfp4_linear_grouped_fwd, "qfp4_linear_grouped_fwd", i, X.data_ptr(), W.data_ptr(), Y.data_ptr(),
+        offsets.data_ptr(), E, T, N, K, ctypes.byref(rec), ctypes.byref(seed),
+        None if x_amax is None else _vector(x_amax, 1, torch.float32, i), wsp, wsb)
     return Y
 
 
-def linear_grouped_bwd(dY, X, W, offsets, rec: Recipe, seed: Seed, dX=None, dW=None, workspace=None, stream=None):
+@_on_stream
+def linear_grouped_bwd(dY, X, W, offsets, rec: Recipe, seed: Seed, dX=None, dW=None, workspace=None):
     """(dX, dW) of linear_grouped_fwd; see qfp4_linear_grouped_bwd. Rows of dX
     that are no group's are not written; dW of an empty group is zero."""
-    T, E, N, K = _linear_grouped_args(X, W, offsets)
-    assert dY.shape == (T, N) and dY.dtype == torch.bfloat16 and dY.is_contiguous() and dY.device == X.device
-    dX = torch.empty((T, K), dtype=_dtype(rec.dx_dtype), device=X.device) if dX is None else dX
-    assert dX.shape == (T, K) and dX.dtype == _dtype(rec.dx_dtype) and dX.is_contiguous() and dX.device == X.device
+    T, E, N, K, i = _linear_grouped_args(X, W, offsets)
+    assert dY.shape == (T, N) and dY.dtype == torch.bfloat16 and dY.is_contiguous() and dY.get_device() == i
+    dX = _linear_output(dX, (T, K), rec.dx_dtype, X)
     if rec.dw_accumulate and dW is None:
         raise ValueError("a recipe with dw_accumulate adds into dW: pass the buffer")
-    dW = torch.empty((E, N, K), dtype=_dtype(rec.dw_dtype), device=X.device) if dW is None else dW
-    assert dW.shape == (E, N, K) and dW.dtype == _dtype(rec.dw_dtype) and dW.is_contiguous() and dW.device == X.device
-    if workspace is None:
-        workspace = torch.empty((linear_grouped_workspace_bytes(True, T, E, N, K, rec),), dtype=torch.uint8,
-                                device=X.device)
-    _check(lib().qfp4_linear_grouped_bwd(_ptr(dY), _ptr(X), _ptr(W), _ptr(dX), _ptr(dW), _ptr(offsets), E, T, N, K,
-                                         ctypes.byref(rec), ctypes.byref(seed), _ptr(workspace), workspace.numel(),
-                                         _stream(stream)), "qfp4_linear_grouped_bwd")
+    dW = _linear_output(dW, (E, N, K), rec.dw_dtype, X)
+    wsp, wsb, workspace = _workspace(workspace, linear_grouped_workspace_bytes(True, T, E, N, K, rec), X)
+    _go(lib().qfp4_linear_grouped_bwd, "qfp4_linear_grouped_bwd", i, dY.data_ptr(), X.data_ptr(),
+        W.data_ptr(), dX.data_ptr(), dW.data_ptr(), offsets.data_ptr(), E, T, N, K, ctypes.byref(rec),
+        ctypes.byref(seed), wsp, wsb)
     return dX, dW
 
 
