@@ -15,8 +15,8 @@
 //
 // The main kernel is the dense CTA-pair kernel (256 x 256 tiles, tcgen05
 // cta_group::2, the same warp roles and rings) with another walk: every role
-// finds a tile's group by a binary search over prefix sums of the tile counts
-// in shared memory, which the CTA builds once from the offsets. A tile never
+// steps through prefix sums of the groups' tile counts in shared memory, which
+// the CTA builds once from the offsets. A tile never
 // spans two groups. Rows of D past a group belong to the next one: 32-row
 // boxes that are full leave by TMA, the one a group's end cuts is written row
 // by row from the registers.
@@ -34,42 +34,47 @@ struct GroupTile {
     int k0, k;   // first element of the reduction in A, its length
 };
 
+// Every role steps through the tiles by itself. In rows mode the groups are
+// walked along with the tiles (a CTA's next tile is rarely more than a group or
+// two ahead), so that no role searches for its group.
 template <bool WGRAD, int TILE_M>
 struct GroupWalk {
     const GroupTable& g;
-    const GroupedParams& p;
-    int num_m, num_n, total;
-    __device__ __forceinline__ GroupWalk(const GroupTable& t, const GroupedParams& q) : g(t), p(q) {
-        num_n = (p.N + kGemmBN - 1) / kGemmBN;
-        num_m = WGRAD ? (p.M + TILE_M - 1) / TILE_M : 0;
-        total = WGRAD ? p.E * num_m * num_n : g.tiles[p.E] * num_n;
+    int e = 0;  // group of the last tile
+    __device__ __forceinline__ explicit GroupWalk(const GroupTable& t) : g(t) {}
+    static __device__ __forceinline__ int num_n(const GroupedParams& p) { return (p.N + kGemmBN - 1) / kGemmBN; }
+    static __device__ __forceinline__ int num_m(const GroupedParams& p) { return (p.M + TILE_M - 1) / TILE_M; }
+    __device__ __forceinline__ int total(const GroupedParams& p) const {
+        return (WGRAD ? p.E * num_m(p) : g.tiles[p.E]) * num_n(p);
     }
-    // Within a group the row tiles run fastest: concurrent CTAs share the
-    // group's B tiles in L2.
-    __device__ __forceinline__ GroupTile at(int t) const {
+    // Tile t < total(), t rising; within a group in the dense kernel's order.
+    __device__ __forceinline__ GroupTile at(const GroupedParams& p, int t) {
         GroupTile r;
+        const int nn = num_n(p);
+        int mb, nb;
         if constexpr (WGRAD) {
-            const int per = num_m * num_n, i = t % per;
-            r.e = t / per;
-            r.m0 = (i % num_m) * TILE_M;
-            r.n0 = (i / num_m) * kGemmBN;
+            const int nm = num_m(p), i = t % (nm * nn);
+            r.e = t / (nm * nn);
+            tile_coords<P_GROUP_M>(i, nm, nn, mb, nb);
             r.k0 = g.padded[r.e];
             r.k = g.padded[r.e + 1] - r.k0;
         } else {
-            r.e = group_of(g.tiles, p.E, t / num_n);
-            const int first = g.tiles[r.e], tm = g.tiles[r.e + 1] - first, i = t - first * num_n;
-            r.m0 = (i % tm) * TILE_M;
-            r.n0 = (i / tm) * kGemmBN;
+            while (t >= g.tiles[e + 1] * nn) ++e;
+            const int first = g.tiles[e], tm = g.tiles[e + 1] - first, i = t - first * nn;
+            r.e = e;
+            tile_coords<P_GROUP_M>(i, tm, nn, mb, nb);
             r.k0 = 0;
             r.k = p.K;
         }
+        r.m0 = mb * TILE_M;
+        r.n0 = nb * kGemmBN;
         return r;
     }
 };
 
 // Rows cut by a group's end: this lane's 32 words (128 bytes) of its row to D
 // from column x, by 16-byte stores (N is a multiple of 8).
-__device__ __forceinline__ void store_row_words(const GroupedParams& p, const uint32_t* v, int64_t row, int x) {
+__device__ __forceinline__ void store_row_words(const GroupedParams& p, const uint32_t* v, int row, int x) {
     const int esz = p.out_f32 ? 4 : 2, per = 16 / esz;
     uint8_t* d = static_cast<uint8_t*>(p.D) + (row * p.ldd + x) * esz;
 #pragma unroll
@@ -86,7 +91,7 @@ __device__ __forceinline__ void store_row_words(const GroupedParams& p, const ui
 // in fp32 after the first 32 are stored.
 template <int NBOX, typename Release>
 __device__ __forceinline__ void group_epilogue(const GroupedParams& p, const CUtensorMap* tmD, uint32_t taddr,
-                                               int64_t row, int nv, int n0, float scale, bool zero, uint32_t obox,
+                                               int row, int nv, int n0, float scale, bool zero, uint32_t obox,
                                                int& turn, int lane, Release release) {
     // 32 words (128 bytes) of each lane's row, from column x: a whole box of 32
     // rows through shared memory (128-byte swizzle) by TMA, which clips the
@@ -108,9 +113,9 @@ __device__ __forceinline__ void group_epilogue(const GroupedParams& p, const CUt
         if (lane == 0) {
             if (x < p.N) {
                 if (p.accumulate)
-                    tma_reduce_add_2d(tmD, buf, x, (int)row);
+                    tma_reduce_add_2d(tmD, buf, x, row);
                 else
-                    tma_store_2d(tmD, buf, x, (int)row);
+                    tma_store_2d(tmD, buf, x, row);
             }
             bulk_commit_group();  // (an empty group keeps the count)
         }
@@ -229,15 +234,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     cluster_sync();  // barriers of both CTAs initialised, tensor memory allocated, groups known
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const GroupWalk<WGRAD, 2 * BM> walk(groups, p);
+    GroupWalk<WGRAD, 2 * BM> walk(groups);
+    const int total = walk.total(p);
 
     if (warp == 0) {
         // ---------------- TMA producer (both CTAs) ----------------
         if (lane == 0) {
             int it = 0;
             bool ok = true;
-            for (int t = cid; t < walk.total && ok; t += nclusters) {
-                const GroupTile w = walk.at(t);
+            for (int t = cid; t < total && ok; t += nclusters) {
+                const GroupTile w = walk.at(p, t);
                 const int arow = (WGRAD ? 0 : groups.padded[w.e]) + w.m0 + (int)rank * BM;
                 const int brow = (WGRAD ? 0 : w.e * p.b_rows) + w.n0;
                 const int bk0 = WGRAD ? w.k0 : w.e * p.b_k;
@@ -266,8 +272,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             int s = 0, lt = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int t = cid; t < walk.total && ok; t += nclusters, ++lt) {
-                const GroupTile w = walk.at(t);
+            for (int t = cid; t < total && ok; t += nclusters, ++lt) {
+                const GroupTile w = walk.at(p, t);
                 if (lt > 0 && !mbar_wait_cluster(acc_empty, (lt - 1) & 1)) break;
                 tc_fence_after();
                 for (int k = 0; k < w.k; k += BK) {
@@ -296,8 +302,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int t = cid; t < walk.total && ok; t += nclusters) {
-            const int k_len = walk.at(t).k;
+        for (int t = cid; t < total && ok; t += nclusters) {
+            const int k_len = walk.at(p, t).k;
             for (int k = 0; k < k_len; k += BK) {
                 if (!mbar_wait_cluster(&sf_load[s], ph)) {
                     ok = false;
@@ -326,17 +332,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
         const uint32_t obox = smem_u32(sOut) + (uint32_t)((warp - kFirstEpiWarp) * BOXES * P_OUT_BOX);
         int lt = 0, turn = 0;
-        for (int t = cid; t < walk.total; t += nclusters, ++lt) {
-            const GroupTile w = walk.at(t);
+        for (int t = cid; t < total; t += nclusters, ++lt) {
+            const GroupTile w = walk.at(p, t);
             if (!mbar_wait_cluster(acc_full, lt & 1)) break;
             tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(lq * 32) << 16) + TMEM_D + chalf * 128;
             const int m = w.m0 + (int)rank * BM + lq * 32;  // within the group
             const int nv = min(32, (WGRAD ? p.M : groups.size(w.e)) - m);
-            const int64_t row = (WGRAD ? (int64_t)w.e * p.M : groups.row[w.e]) + m;
+            const int row = (WGRAD ? w.e * p.M : groups.row[w.e]) + m;
             // an empty group's weight gradient is zero; added to D it changes nothing
-            group_epilogue<BOXES>(p, &tmD, taddr, row, w.k == 0 && p.accumulate ? 0 : nv, w.n0 + chalf * 128, scale,
-                                  w.k == 0, obox, turn, lane, [&] {
+            const bool zero = WGRAD && w.k == 0;
+            group_epilogue<BOXES>(p, &tmD, taddr, row, zero && p.accumulate ? 0 : nv, w.n0 + chalf * 128, scale, zero,
+                                  obox, turn, lane, [&] {
                                       if (lane == 0) mbar_arrive_cluster(acc_empty_leader);
                                   });
         }
@@ -405,15 +412,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const GroupWalk<false, BM> walk(groups, p);
+    GroupWalk<false, BM> walk(groups);
+    const int total = walk.total(p);
 
     if (warp == 0) {
         // ---------------- TMA producer ----------------
         if (lane == 0) {
             int it = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < walk.total && ok; t += gridDim.x) {
-                const GroupTile w = walk.at(t);
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+                const GroupTile w = walk.at(p, t);
                 const int arow = groups.padded[w.e] + w.m0, brow = w.e * p.b_rows + w.n0, bk0 = w.e * p.b_k;
                 const int nrb = (w.n0 + 128 < p.N) ? 2 : 1;  // B row blocks of this group
                 for (int kt = 0; kt < KT; ++kt, ++it) {
@@ -445,7 +453,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             int s = 0, lt = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < walk.total && ok; t += gridDim.x, ++lt) {
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++lt) {
                 if (lt > 0 && !mbar_wait(acc_empty, (lt - 1) & 1)) break;
                 tc_fence_after();
                 for (int kt = 0; kt < KT; ++kt) {
@@ -474,7 +482,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < walk.total && ok; t += gridDim.x) {
+        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
             for (int kt = 0; kt < KT; ++kt) {
                 if (!mbar_wait(&sf_load[s], ph)) {
                     ok = false;
@@ -501,14 +509,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int chalf = (warp - kFirstEpiWarp) >> 2;
         const float scale = __fmul_rn(__ldg(p.ga), __ldg(p.gb));
         int lt = 0;
-        for (int t = blockIdx.x; t < walk.total; t += gridDim.x, ++lt) {
-            const GroupTile w = walk.at(t);
+        for (int t = blockIdx.x; t < total; t += gridDim.x, ++lt) {
+            const GroupTile w = walk.at(p, t);
             if (!mbar_wait(acc_full, lt & 1)) break;
             tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(lq * 32) << 16) + TMEM_D + chalf * 128;
             const int m = w.m0 + lq * 32 + lane, n0 = w.n0 + chalf * 128;
             const bool mine = m < groups.size(w.e);
-            const int64_t row = groups.row[w.e] + m;
+            const int row = groups.row[w.e] + m;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t acc[64];
