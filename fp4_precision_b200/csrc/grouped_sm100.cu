@@ -85,39 +85,35 @@ __device__ __forceinline__ void store_row_words(const GroupedParams& p, const ui
 }
 
 // Epilogue of one tile for one warp: 32 rows x 128 columns from D row `row`, nv
-// of the rows stored; zero: the sum of an empty group. The warp has NBOX boxes
-// of shared memory in turn. The accumulator goes back to the MMA warp as soon
-// as the values are in registers: all 128 columns packed to bf16, or the last 96
-// in fp32 after the first 32 are stored.
-template <int NBOX, typename Release>
-__device__ __forceinline__ void group_epilogue(const GroupedParams& p, const CUtensorMap* tmD, uint32_t taddr,
-                                               int row, int nv, int n0, float scale, bool zero, uint32_t obox,
-                                               int& turn, int lane, Release release) {
+// of the rows stored; zero: the sum of an empty group. The accumulator goes back
+// to the MMA warp as soon as the values are in registers: all 128 columns
+// packed to bf16, or the last 96 in fp32 after the first 32 are stored.
+template <typename Release>
+__device__ __forceinline__ void group_epilogue(const GroupedParams& p, const CUtensorMap* tmD, uint32_t taddr, int row,
+                                               int nv, int n0, float scale, bool zero, uint32_t obox, int lane,
+                                               Release release) {
     // 32 words (128 bytes) of each lane's row, from column x: a whole box of 32
     // rows through shared memory (128-byte swizzle) by TMA, which clips the
     // columns past N
+    const uint32_t rbase = obox + (uint32_t)lane * 128u;
     auto box = [&](const uint32_t* v, int x) {
         if (nv < 32) {
             if (lane < nv) store_row_words(p, v, row + lane, x);
             return;
         }
-        const uint32_t buf = obox + (uint32_t)turn * P_OUT_BOX, rbase = buf + (uint32_t)lane * 128u;
-        if (++turn == NBOX) turn = 0;
-        if (lane == 0) bulk_wait_group_read<NBOX - 1>();  // the box's last store has read it
+        if (lane == 0) bulk_wait_group_read0();  // the box's last store has read it
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             sts128(rbase + ((uint32_t)(j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0) {
-            if (x < p.N) {
-                if (p.accumulate)
-                    tma_reduce_add_2d(tmD, buf, x, row);
-                else
-                    tma_store_2d(tmD, buf, x, row);
-            }
-            bulk_commit_group();  // (an empty group keeps the count)
+        if (lane == 0 && x < p.N) {
+            if (p.accumulate)
+                tma_reduce_add_2d(tmD, obox, x, row);
+            else
+                tma_store_2d(tmD, obox, x, row);
+            bulk_commit_group();
         }
     };
     if (!p.out_f32) {
@@ -166,16 +162,13 @@ __device__ __forceinline__ void group_epilogue(const GroupedParams& p, const CUt
     }
 }
 
-// Ring stages and boxes per epilogue warp. The weight gradient's sums are short
-// (a group's tokens) and its outputs fp32, so its stores weigh more: two boxes
-// per warp for one stage less.
-template <bool WGRAD>
-struct GroupPipe {
-    static constexpr int kStages = WGRAD ? 4 : P_STAGES;
-    static constexpr int kBoxes = WGRAD ? 2 : 1;
-    static constexpr int kBytes = kStages * P_STAGE + kEpiWarps * kBoxes * P_OUT_BOX + 1024 + 512 + (int)sizeof(GroupTable);
-    static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
-};
+// Five ring stages and one box per epilogue warp, as the dense kernel. The
+// weight gradient's sums are short (a group's tokens) and its stores heavy, yet
+// the operand loads want the stages more than the stores boxes: 16 groups of
+// 1024 tokens, 2816 x 2048 in fp32, 81.7 us; 4 stages and 2 boxes 85.5; 3 and 3
+// 103.6 (4.5 TB/s of output; a plain fill of memory reaches 3.7 here).
+constexpr int GP_SMEM = P_SMEM + (int)sizeof(GroupTable);
+static_assert(GP_SMEM <= 227 * 1024, "shared memory of one CTA");
 
 template <int FMT, bool WGRAD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
@@ -186,23 +179,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     constexpr int ATOMS_PER_KT = BK / SF_K;  // 4 or 2
     constexpr uint32_t AB_TX = 2u * (P_A + P_B);          // both CTAs, on the leader
     constexpr uint32_t SF_TX = 3u * ATOMS_PER_KT * 512u;  // this CTA's scale boxes
-    constexpr int ST = GroupPipe<WGRAD>::kStages, BOXES = GroupPipe<WGRAD>::kBoxes;
     extern __shared__ __align__(1024) uint8_t dyn_smem[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = base;
-    uint8_t* sB = sA + ST * P_A;
-    uint8_t* sSFA = sB + ST * P_B;
-    uint8_t* sSFB = sSFA + ST * P_SFA;
-    uint8_t* sOut = sSFB + ST * P_SFB;  // kEpiWarps boxes, 1024-byte aligned
-    uint64_t* full = reinterpret_cast<uint64_t*>(sOut + kEpiWarps * BOXES * P_OUT_BOX);
-    uint64_t* empty = full + ST;
-    uint64_t* sf_load = empty + ST;    // this CTA's scale atoms of stage s landed
-    uint64_t* sf_full = sf_load + ST;  // scale slot s written in both CTAs (leader's)
-    uint64_t* acc_full = sf_full + ST;
+    uint8_t* sB = sA + P_STAGES * P_A;
+    uint8_t* sSFA = sB + P_STAGES * P_B;
+    uint8_t* sSFB = sSFA + P_STAGES * P_SFA;
+    uint8_t* sOut = sSFB + P_STAGES * P_SFB;  // kEpiWarps boxes, 1024-byte aligned
+    uint64_t* full = reinterpret_cast<uint64_t*>(sOut + kEpiWarps * P_OUT_BOX);
+    uint64_t* empty = full + P_STAGES;
+    uint64_t* sf_load = empty + P_STAGES;    // this CTA's scale atoms of stage s landed
+    uint64_t* sf_full = sf_load + P_STAGES;  // scale slot s written in both CTAs (leader's)
+    uint64_t* acc_full = sf_full + P_STAGES;
     uint64_t* acc_empty = acc_full + 1;
     uint64_t* drain = acc_empty + 1;  // every MMA the leader issued has completed (both CTAs)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-    GroupTable& groups = *reinterpret_cast<GroupTable*>(sOut + kEpiWarps * BOXES * P_OUT_BOX + 512);
+    GroupTable& groups = *reinterpret_cast<GroupTable*>(sOut + kEpiWarps * P_OUT_BOX + 512);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -214,7 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         prefetch_tmap(&tmSFA);
         prefetch_tmap(&tmSFB);
         prefetch_tmap(&tmD);
-        for (int s = 0; s < ST; ++s) {
+        for (int s = 0; s < P_STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
             mbar_init(&sf_load[s], 1);
@@ -249,8 +241,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                 const int bk0 = WGRAD ? w.k0 : w.e * p.b_k;
                 const int kt_n = (w.k + BK - 1) / BK;
                 for (int kt = 0; kt < kt_n; ++kt, ++it) {
-                    const int s = it % ST;
-                    if (it >= ST && !mbar_wait_cluster(&empty[s], ((it / ST) + 1) & 1)) {
+                    const int s = it % P_STAGES;
+                    if (it >= P_STAGES && !mbar_wait_cluster(&empty[s], ((it / P_STAGES) + 1) & 1)) {
                         ok = false;
                         break;
                     }
@@ -263,7 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                     tma_load_2d_pair(sB + s * P_B, &tmB, bar_leader, bk0 / 2 + kt * (BK / 2), brow + (int)rank * 128);
                 }
             }
-            drain_loads(rank == 0 ? full : nullptr, sf_load, ST, it);
+            drain_loads(rank == 0 ? full : nullptr, sf_load, P_STAGES, it);
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer (leader CTA only) ----------------
@@ -286,7 +278,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                                                  b_desc0 + (uint64_t)(s * (P_B >> 4)), tmem + sfa_col(s),
                                                  tmem + sfb_col(s), min(BK, w.k - k) / 64, k == 0);
                     tc_commit_pair(&empty[s]);  // frees stage s and scale slot s in both CTAs
-                    if (++s == ST) {
+                    if (++s == P_STAGES) {
                         s = 0;
                         ph ^= 1;
                     }
@@ -318,7 +310,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sf_full[s]), 0));
-                if (++s == ST) {
+                if (++s == P_STAGES) {
                     s = 0;
                     ph ^= 1;
                 }
@@ -330,8 +322,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const int chalf = (warp - kFirstEpiWarp) >> 2;
         const float scale = __fmul_rn(__ldg(p.ga), __ldg(p.gb));
         const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
-        const uint32_t obox = smem_u32(sOut) + (uint32_t)((warp - kFirstEpiWarp) * BOXES * P_OUT_BOX);
-        int lt = 0, turn = 0;
+        const uint32_t obox = smem_u32(sOut) + (uint32_t)(warp - kFirstEpiWarp) * P_OUT_BOX;
+        int lt = 0;
         for (int t = cid; t < total; t += nclusters, ++lt) {
             const GroupTile w = walk.at(p, t);
             if (!mbar_wait_cluster(acc_full, lt & 1)) break;
@@ -342,10 +334,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             const int row = (WGRAD ? w.e * p.M : groups.row[w.e]) + m;
             // an empty group's weight gradient is zero; added to D it changes nothing
             const bool zero = WGRAD && w.k == 0;
-            group_epilogue<BOXES>(p, &tmD, taddr, row, zero && p.accumulate ? 0 : nv, w.n0 + chalf * 128, scale, zero,
-                                  obox, turn, lane, [&] {
-                                      if (lane == 0) mbar_arrive_cluster(acc_empty_leader);
-                                  });
+            group_epilogue(p, &tmD, taddr, row, zero && p.accumulate ? 0 : nv, w.n0 + chalf * 128, scale, zero, obox,
+                           lane, [&] {
+                               if (lane == 0) mbar_arrive_cluster(acc_empty_leader);
+                           });
         }
         if (lane == 0) bulk_wait_group0();  // this warp's stores are complete
     }
@@ -573,11 +565,10 @@ cudaError_t launch_gemm_grouped(const GroupedParams& p, int fmt, bool wgrad, boo
     }
     const int64_t num_m = wgrad ? (int64_t)p.E * ((p.M + 255) / 256) : std::min<int64_t>(p.T, p.T / 256 + p.E);
     const int clusters = (int)std::max<int64_t>(1, std::min<int64_t>(sms / 2, num_m * num_n));
-    const int smem = wgrad ? GroupPipe<true>::kBytes : GroupPipe<false>::kBytes;
     auto run = [&](auto* kern) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GP_SMEM);
         if (e != cudaSuccess) return e;
-        return launch_pdl(kern, dim3(2 * clusters), dim3(kGemmThreads), smem, s, *tmapA, *tmapB, *tmapSFA, *tmapSFB,
+        return launch_pdl(kern, dim3(2 * clusters), dim3(kGemmThreads), GP_SMEM, s, *tmapA, *tmapB, *tmapSFA, *tmapSFB,
                           *tmapD, p);
     };
     cudaError_t e;

@@ -13,54 +13,79 @@
 // c) + dh), dw = sum over the rows of dy * h * rstd, all in fp32.
 //
 // Both are bound by HBM: every tensor crosses it once, a row stays in
-// registers between the sum and its use. A row belongs to one CTA (C > 1024)
-// or one warp; a thread holds 32 elements of it, whole Hadamard groups, so
-// that the rotation needs no shuffles. CTAs are persistent: the weight is
-// loaded once, and the next row's loads are issued before the row's sum is
-// joined. The backward pass of wide rows has them arrive through a ring in
-// shared memory.
+// registers between the sum and its use. A row belongs to one CTA, or, narrow
+// ones, to one warp. Forward, a thread holds 16 or 32 elements of it, whole
+// Hadamard groups and blocks, so that the rotation needs no shuffles; backward
+// 16, and the weight gradient of its columns. CTAs are persistent: the weight
+// is loaded once, and rows arrive ahead of their turn, forward in registers,
+// backward (wide ones) by bulk copies into a ring in shared memory.
 #include "qfp4_device.cuh"
 #include "qfp4_internal.h"
 
 namespace qfp4 {
 namespace {
 
-constexpr int kNormElems = 32;        // elements of a row per thread
-constexpr int kNormWarpRowC = 1024;   // up to this many columns a row belongs to one warp
-constexpr int kNormMaxThreads = 512;  // C <= 16384
-constexpr int kNormMaxStages = 4;     // rows in flight per CTA of the backward ring
+constexpr int kNormWarpRowC = 512;  // up to this many columns a row belongs to one warp (backward)
+constexpr int kNormMaxStages = 4;   // rows in flight per CTA
 constexpr int kNormRingBytes = 192 * 1024;
 
-// A thread's 32 elements are NCH chunks of G consecutive ones (G = 16: chunks
-// t and t + threads per row; G = 32: chunk t).
-template <int G>
+// 32 bytes of one thread, whole DRAM sectors in one instruction (32-byte aligned).
+__device__ __forceinline__ void ldg256(const void* p, uint32_t* w) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void stg256(void* p, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "l"(p)
+                 : "memory");
+}
+
+// A thread's part of a row: chunks t and (NCH = 2) t + threads of G elements.
+template <int G, int NCH>
 struct NormChunks {
-    static constexpr int NCH = kNormElems / G;
-    int tpr, t;     // threads per row, this thread's index among them
-    int chunks;     // chunks in a row
+    static constexpr int WORDS = G / 2 * NCH;
+    int tpr, t;  // threads per row, this thread's index among them
+    int chunks;  // chunks in a row
+    bool wide;   // rows are 32-byte aligned
     __device__ __forceinline__ bool has(int i) const { return t + i * tpr < chunks; }
-    __device__ __forceinline__ int64_t at(int i) const { return (int64_t)(t + i * tpr) * G; }
-    // 16 words of packed bf16 pairs; chunks past the row are zero
+    __device__ __forceinline__ int at(int i) const { return (t + i * tpr) * G; }
+    // packed bf16 pairs; chunks past the row are zero
     __device__ __forceinline__ void load(const uint16_t* row, uint32_t* w) const {
 #pragma unroll
         for (int i = 0; i < NCH; ++i)
 #pragma unroll
-            for (int v = 0; v < G / 8; ++v) {
-                uint4 q = make_uint4(0, 0, 0, 0);
-                if (has(i)) q = *reinterpret_cast<const uint4*>(row + at(i) + 8 * v);
-                uint32_t* d = w + i * (G / 2) + 4 * v;
-                d[0] = q.x; d[1] = q.y; d[2] = q.z; d[3] = q.w;
+            for (int v = 0; v < G / 16; ++v) {
+                uint32_t* d = w + i * (G / 2) + 8 * v;
+                const uint16_t* src = row + at(i) + 16 * v;
+                if (!has(i)) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) d[k] = 0;
+                } else if (wide) {
+                    ldg256(src, d);
+                } else {
+                    const uint4 q0 = reinterpret_cast<const uint4*>(src)[0], q1 = reinterpret_cast<const uint4*>(src)[1];
+                    d[0] = q0.x; d[1] = q0.y; d[2] = q0.z; d[3] = q0.w;
+                    d[4] = q1.x; d[5] = q1.y; d[6] = q1.z; d[7] = q1.w;
+                }
             }
     }
     __device__ __forceinline__ void store(uint16_t* row, const uint32_t* w, const void* base, int64_t extent) const {
 #pragma unroll
         for (int i = 0; i < NCH; ++i)
 #pragma unroll
-            for (int v = 0; v < G / 8; ++v) {
-                const uint32_t* s = w + i * (G / 2) + 4 * v;
-                if (has(i))
-                    *chk(reinterpret_cast<uint4*>(row + at(i) + 8 * v), base, extent) =
-                        make_uint4(s[0], s[1], s[2], s[3]);
+            for (int v = 0; v < G / 16; ++v) {
+                const uint32_t* d = w + i * (G / 2) + 8 * v;
+                uint16_t* dst = row + at(i) + 16 * v;
+                if (!has(i)) continue;
+                if (wide) {
+                    stg256(chk(dst, base, extent, 32), d);
+                } else {
+                    uint4* q = reinterpret_cast<uint4*>(dst);
+                    *chk(q, base, extent) = make_uint4(d[0], d[1], d[2], d[3]);
+                    *chk(q + 1, base, extent) = make_uint4(d[4], d[5], d[6], d[7]);
+                }
             }
     }
 };
@@ -71,76 +96,50 @@ __device__ __forceinline__ uint32_t norm_pack(float lo, float hi) {
 }
 __device__ __forceinline__ int64_t rows_extent(int64_t R, int64_t C, int64_t ld) { return R <= 0 ? 0 : ((R - 1) * ld + C) * 2; }
 
-// Sum over the threads of a row, the same in each of them: shuffles, then (a
-// row of several warps) one barrier; `red` alternates between two halves, so
-// that the next row's partial sums do not overtake this one's.
-template <bool WARP_ROW, typename T>
-__device__ __forceinline__ T norm_row_sum(T v, T (*red)[kNormMaxThreads / 32], int parity) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if constexpr (!WARP_ROW) {
-        const int warps = blockDim.x >> 5;
-        if ((threadIdx.x & 31) == 0) red[parity][threadIdx.x >> 5] = v;
-        __syncthreads();
-        v = red[parity][0];
-        for (int w = 1; w < warps; ++w) v += red[parity][w];
-    }
-    return v;
-}
-
+// ---- forward -------------------------------------------------------------------
 // NH: -1 no amax, else the Hadamard size of the amax or (QUANT) of the MXFP4
 // quantization.
-template <int NH, bool QUANT, bool WARP_ROW>
-__global__ void __launch_bounds__(WARP_ROW ? 128 : kNormMaxThreads) rmsnorm_fwd_kernel(const NormParams p) {
-    constexpr int G = (QUANT || NH == 32) ? 32 : 16;
-    using Chunks = NormChunks<G>;
-    __shared__ double red[2][kNormMaxThreads / 32];
-    __shared__ float red_max[kNormMaxThreads / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t owners = WARP_ROW ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
-    const int64_t first = WARP_ROW ? (int64_t)blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
-    const Chunks ch{WARP_ROW ? 32 : (int)blockDim.x, WARP_ROW ? lane : (int)threadIdx.x, (int)(p.C / G)};
-    pdl_wait();  // the previous kernel's writes are visible (and its reads done)
-    pdl_launch_dependents();
-
-    const int64_t rows_padded = QUANT ? (p.R + 127) / 128 * 128 : p.R;  // scale rows up to the atom are zero
-    uint32_t xw[16], rw[16], ww[16];
-    ch.load(p.w, ww);
-    if (first < p.R) {
-        ch.load(p.x + first * p.ldx, xw);
-        if (p.res != nullptr) ch.load(p.res + first * p.ldres, rw);
-    }
-    if (QUANT && blockIdx.x == 0 && threadIdx.x == 0) *chk(p.q_tensor_scale, p.q_tensor_scale, 4) = 1.0f;
+template <int NH, bool QUANT>
+constexpr int kNormChunk = (QUANT || NH == 32) ? 32 : 16;  // whole Hadamard groups and MXFP4 blocks
+template <int NH, bool QUANT, int NCH>
+struct NormFwd {
+    static constexpr int G = kNormChunk<NH, QUANT>;
+    static_assert(G == 16 || NCH == 1, "32 elements at most");
+    using Chunks = NormChunks<G, NCH>;
+    static constexpr int WORDS = Chunks::WORDS;
+    Chunks ch;
+    uint32_t ww[WORDS];
     float amax = 0.0f;
-    int parity = 0;
-    for (int64_t row = first; row < rows_padded; row += owners, parity ^= 1) {
-        uint32_t hw[16];
-        float rstd = 0.0f;
-        if (row < p.R) {
-            double ss = 0.0;
+
+    // h = x + r of this thread's elements, stored, and the sum of its squares.
+    __device__ __forceinline__ double residual(const NormParams& p, int64_t row, const uint32_t* xw, const uint32_t* rw,
+                                               uint32_t* hw) const {
+        double ss = 0.0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                hw[i] = p.res != nullptr ? norm_pack(__fadd_rn(bf16lo(xw[i]), bf16lo(rw[i])),
-                                                     __fadd_rn(bf16hi(xw[i]), bf16hi(rw[i])))
-                                         : xw[i];
-                const double a = bf16lo(hw[i]), b = bf16hi(hw[i]);
-                ss = __fma_rn(a, a, ss);
-                ss = __fma_rn(b, b, ss);
-            }
-            if (p.h != nullptr) ch.store(p.h + row * p.ldh, hw, p.h, rows_extent(p.R, p.C, p.ldh));
-            if (row + owners < p.R) {  // the next row's loads, under this row's sum and outputs
-                ch.load(p.x + (row + owners) * p.ldx, xw);
-                if (p.res != nullptr) ch.load(p.res + (row + owners) * p.ldres, rw);
-            }
-            ss = norm_row_sum<WARP_ROW>(ss, red, parity);
-            rstd = (float)rsqrt(ss * p.inv_c + p.eps);
-            if (ch.t == 0) *chk(p.rstd + row, p.rstd, p.R * 4) = rstd;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                hw[i] = norm_pack(__fmul_rn(__fmul_rn(bf16lo(hw[i]), rstd), bf16lo(ww[i])),
-                                  __fmul_rn(__fmul_rn(bf16hi(hw[i]), rstd), bf16hi(ww[i])));
-            if (!QUANT || p.y != nullptr) ch.store(p.y + row * p.ldy, hw, p.y, rows_extent(p.R, p.C, p.ldy));
+        for (int i = 0; i < WORDS; ++i) {
+            hw[i] = p.res != nullptr ? norm_pack(__fadd_rn(bf16lo(xw[i]), bf16lo(rw[i])),
+                                                 __fadd_rn(bf16hi(xw[i]), bf16hi(rw[i])))
+                                     : xw[i];
+            const double a = bf16lo(hw[i]), b = bf16hi(hw[i]);
+            ss = __fma_rn(a, a, ss);
+            ss = __fma_rn(b, b, ss);
         }
+        if (p.h != nullptr) ch.store(p.h + row * p.ldh, hw, p.h, rows_extent(p.R, p.C, p.ldh));
+        return ss;
+    }
+    // y from h and the row's sum of squares, stored; in hw's place.
+    __device__ __forceinline__ void normalize(const NormParams& p, int64_t row, uint32_t* hw, double ss) const {
+        const float rstd = (float)rsqrt(ss * p.inv_c + p.eps);
+        if (ch.t == 0) *chk(p.rstd + row, p.rstd, p.R * 4) = rstd;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i)
+            hw[i] = norm_pack(__fmul_rn(__fmul_rn(bf16lo(hw[i]), rstd), bf16lo(ww[i])),
+                              __fmul_rn(__fmul_rn(bf16hi(hw[i]), rstd), bf16hi(ww[i])));
+        if (!QUANT || p.y != nullptr) ch.store(p.y + row * p.ldy, hw, p.y, rows_extent(p.R, p.C, p.ldy));
+    }
+    // y's amax or quantization; rows from R on (up to the scale atom's 128) get
+    // zero scales.
+    __device__ __forceinline__ void output(const NormParams& p, int64_t row, const uint32_t* yw) {
         if constexpr (QUANT) {
             using Grp = Group<kMxfp4, kRtn, NH>;
             static_assert(Grp::G == 32, "32-element MXFP4 blocks");
@@ -151,7 +150,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 128 : kNormMaxThreads) rmsnorm_fwd_
                 float v[32];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    uint32_t x = hw[i];
+                    uint32_t x = yw[i];
                     if (NH > 0 && p.signs != 0u) x ^= Grp::sign_mask(p.signs, i);
                     v[2 * i] = bf16lo(x);
                     v[2 * i + 1] = bf16hi(x);
@@ -175,11 +174,11 @@ __global__ void __launch_bounds__(WARP_ROW ? 128 : kNormMaxThreads) rmsnorm_fwd_
         } else if constexpr (NH >= 0) {
             using Grp = Group<kNvfp4, kRtn, NH>;
 #pragma unroll
-            for (int i = 0; i < Chunks::NCH; ++i) {
+            for (int i = 0; i < NCH; ++i) {
                 float v[G];
 #pragma unroll
                 for (int k = 0; k < G / 2; ++k) {
-                    uint32_t x = hw[i * (G / 2) + k];
+                    uint32_t x = yw[i * (G / 2) + k];
                     if (NH > 0 && p.signs != 0u) x ^= Grp::sign_mask(p.signs, k);
                     v[2 * k] = bf16lo(x);
                     v[2 * k + 1] = bf16hi(x);
@@ -188,18 +187,87 @@ __global__ void __launch_bounds__(WARP_ROW ? 128 : kNormMaxThreads) rmsnorm_fwd_
             }
         }
     }
-    if constexpr (!QUANT && NH >= 0) {  // the CTA's maximum; c * max |y| = max |c * y|
-        if constexpr (NH > 0) amax = __fmul_rn(amax, had_norm<NH>());
+    // The CTA's maximum; c * max |y| = max |c * y|.
+    __device__ __forceinline__ void finish(const NormParams& p, float* red_max) {
+        if constexpr (!QUANT && NH >= 0) {
+            if constexpr (NH > 0) amax = __fmul_rn(amax, had_norm<NH>());
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if (lane == 0) red_max[warp] = amax;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int w = 1; w < (int)(blockDim.x >> 5); ++w) amax = fmaxf(amax, red_max[w]);
-            *chk(p.amax_out + blockIdx.x, p.amax_out, (int64_t)gridDim.x * 4) = amax;
+            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            if ((threadIdx.x & 31) == 0) red_max[threadIdx.x >> 5] = amax;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                for (int w = 1; w < (int)(blockDim.x >> 5); ++w) amax = fmaxf(amax, red_max[w]);
+                *chk(p.amax_out + blockIdx.x, p.amax_out, (int64_t)gridDim.x * 4) = amax;
+            }
         }
     }
+    // Rows to walk: with the quantization up to the scale atom's 128.
+    static __device__ __forceinline__ int64_t rows(const NormParams& p) {
+        return QUANT ? (p.R + 127) / 128 * 128 : p.R;
+    }
+};
+
+// A row belongs to one warp (WARP_ROW) or one CTA; its loads go straight to
+// registers, the next row's before this row's sum is joined.
+template <int NH, bool QUANT, int NCH, bool WARP_ROW>
+__global__ void __launch_bounds__(WARP_ROW ? 128 : 512) rmsnorm_fwd_kernel(const NormParams p) {
+    using Fwd = NormFwd<NH, QUANT, NCH>;
+    __shared__ double red[2][16];
+    __shared__ float red_max[16];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int64_t owners = WARP_ROW ? (int64_t)gridDim.x * warps : gridDim.x;
+    const int64_t first = WARP_ROW ? (int64_t)blockIdx.x * warps + warp : blockIdx.x;
+    Fwd f;
+    f.ch = typename Fwd::Chunks{WARP_ROW ? 32 : (int)blockDim.x, WARP_ROW ? lane : (int)threadIdx.x,
+                                (int)(p.C / Fwd::G), p.wide != 0};
+    pdl_wait();  // the previous kernel's writes are visible (and its reads done)
+    pdl_launch_dependents();
+    uint32_t xw[Fwd::WORDS], rw[Fwd::WORDS];
+    f.ch.load(p.w, f.ww);
+    if (first < p.R) {
+        f.ch.load(p.x + first * p.ldx, xw);
+        if (p.res != nullptr) f.ch.load(p.res + first * p.ldres, rw);
+    }
+    if (QUANT && blockIdx.x == 0 && threadIdx.x == 0) *chk(p.q_tensor_scale, p.q_tensor_scale, 4) = 1.0f;
+    int parity = 0;
+    for (int64_t row = first; row < Fwd::rows(p); row += owners, parity ^= 1) {
+        uint32_t hw[Fwd::WORDS];
+        if (row < p.R) {
+            double ss = f.residual(p, row, xw, rw, hw);
+            if (row + owners < p.R) {
+                f.ch.load(p.x + (row + owners) * p.ldx, xw);
+                if (p.res != nullptr) f.ch.load(p.res + (row + owners) * p.ldres, rw);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if constexpr (!WARP_ROW) {
+                // two halves in turn: the next row's sums do not overtake this one's
+                if (lane == 0) red[parity][warp] = ss;
+                __syncthreads();
+                ss = red[parity][0];
+                for (int w = 1; w < warps; ++w) ss += red[parity][w];
+            }
+            f.normalize(p, row, hw, ss);
+        }
+        f.output(p, row, hw);
+    }
+    f.finish(p, red_max);
 }
+
+// Rows in flight: a ring of p.stages shared-memory stages that bulk copies
+// fill with one row each of up to three tensors.
+struct NormRing {
+    uint64_t full[kNormMaxStages];
+    int dead;  // a wait ran out
+    __device__ __forceinline__ void init(int stages) {
+        if (threadIdx.x == 0) {
+            for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+            fence_mbarrier_init();
+            dead = 0;
+        }
+        __syncthreads();
+    }
+};
 
 // ---- backward ------------------------------------------------------------------
 // A thread holds up to NV chunks of eight columns (chunks t, t + threads, ...)
@@ -316,25 +384,19 @@ __global__ void __launch_bounds__(128, 4) rmsnorm_bwd_warp_kernel(const NormBwdP
 template <int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) rmsnorm_bwd_ring_kernel(const NormBwdParams p) {
     extern __shared__ __align__(1024) uint8_t dyn_smem[];
-    __shared__ uint64_t full[kNormMaxStages];
+    __shared__ NormRing ring;
     __shared__ float red[2][32];
-    __shared__ int dead;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const uint32_t row_bytes = (uint32_t)p.C * 2, parts = p.dh != nullptr ? 3 : 2;
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
-        fence_mbarrier_init();
-        dead = 0;
-    }
-    __syncthreads();
+    ring.init(p.stages);
     pdl_wait();
     pdl_launch_dependents();
     auto fetch = [&](int64_t row, int s) {  // one thread
         uint8_t* d = dyn_smem + s * parts * row_bytes;
-        mbar_arrive_expect_tx(&full[s], parts * row_bytes);
-        bulk_load(d, p.dy + row * p.lddy, row_bytes, &full[s]);
-        bulk_load(d + row_bytes, p.h + row * p.ldh, row_bytes, &full[s]);
-        if (p.dh != nullptr) bulk_load(d + 2 * row_bytes, p.dh + row * p.lddh, row_bytes, &full[s]);
+        mbar_arrive_expect_tx(&ring.full[s], parts * row_bytes);
+        bulk_load(d, p.dy + row * p.lddy, row_bytes, &ring.full[s]);
+        bulk_load(d + row_bytes, p.h + row * p.ldh, row_bytes, &ring.full[s]);
+        if (p.dh != nullptr) bulk_load(d + 2 * row_bytes, p.dh + row * p.lddh, row_bytes, &ring.full[s]);
     };
     if (threadIdx.x == 0)
         for (int s = 0; s < p.stages && blockIdx.x + (int64_t)s * gridDim.x < p.R; ++s)
@@ -347,7 +409,7 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_bwd_ring_kernel(const NormBwd
     for (int64_t row = blockIdx.x; row < p.R; row += gridDim.x, parity ^= 1) {
         const float rstd = rstd1;
         if (row + gridDim.x < p.R) rstd1 = p.rstd[row + gridDim.x];
-        if (!mbar_wait(&full[s], phase)) dead = 1;  // seen by all behind the barrier
+        if (!mbar_wait(&ring.full[s], phase)) ring.dead = 1;  // seen by all behind the barrier
         const uint16_t* d = reinterpret_cast<const uint16_t*>(dyn_smem + s * parts * row_bytes);
         uint32_t dy[4 * NV], h[4 * NV], dh[4 * NV];
         th.load(d, dy);
@@ -358,7 +420,7 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_bwd_ring_kernel(const NormBwd
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) red[parity][warp] = sum;
         __syncthreads();  // the sums are written, and the stage is read
-        if (dead) break;
+        if (ring.dead) break;
         if (threadIdx.x == 0 && row + (int64_t)p.stages * gridDim.x < p.R) fetch(row + (int64_t)p.stages * gridDim.x, s);
         sum = red[parity][0];
         for (int w = 1; w < warps; ++w) sum += red[parity][w];
@@ -395,50 +457,64 @@ __global__ void __launch_bounds__(1024) norm_dw_reduce_kernel(const float* parti
     if (col == 0 && cw < C) *chk(dw + cw, dw, C * 4) = accumulate ? __fadd_rn(dw[cw], s) : s;
 }
 
-// Threads of a CTA and CTAs for R rows of C columns: as many as the SMs hold
-// at once, at most `most` row owners (0: no such limit).
-void norm_grid(int64_t R, int64_t C, int sms, int64_t most, int* threads, int* grid) {
-    const bool warp_row = C <= kNormWarpRowC;
-    const int64_t t = (C / kNormElems + (C % kNormElems != 0) + 31) / 32 * 32;
-    const int64_t per_cta = warp_row ? 4 : 1;
-    *threads = warp_row ? 128 : (int)t;
-    int64_t g = (R + per_cta - 1) / per_cta;
-    const int64_t fit = (int64_t)sms * std::max(1, 512 / *threads);
-    g = std::min(g, fit);
-    if (most > 0) g = std::min(g, most / per_cta);
-    *grid = g < 1 ? 1 : (int)g;
+// Stages of one CTA's ring, per_sm CTAs sharing the SM's shared memory.
+int norm_stages(int per_sm, int stage_bytes) { return std::min(kNormMaxStages, kNormRingBytes / per_sm / stage_bytes); }
+
+template <typename Kern, typename Params>
+cudaError_t launch_norm_ring(Kern kern, int grid, int threads, int smem, const Params& p, cudaStream_t s) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRingBytes);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(grid), dim3(threads), (size_t)smem, s, p);
 }
 
-template <int NH, bool QUANT>
-cudaError_t launch_norm_fwd_t(const NormParams& p, int threads, int grid, cudaStream_t s) {
+// 768 threads per SM with 16 elements each (68-80 registers), 512 with 32
+// (about 124), and no more CTAs than amax partials. 16 elements and 32-byte
+// accesses measured best on 16384 x 4096 with the amax: 85.5 us; 90.7 with 32
+// elements, 90.3 with 16-byte accesses, 99 with the rows in a ring as in the
+// backward pass (here half the traffic is stores, and more loads in flight
+// delay them).
+template <int NH, bool QUANT, int NCH>
+cudaError_t launch_norm_fwd_t(NormParams p, float* amax, int sms, int* n_partials, cudaStream_t s) {
+    constexpr int G = kNormChunk<NH, QUANT>;
+    const int64_t rows = QUANT ? (p.R + 127) / 128 * 128 : p.R;
+    const bool warp_row = p.C <= 32 * G;
+    const int threads = warp_row ? 128 : (int)((p.C / (G * NCH) + 31) / 32 * 32);
+    const int per_sm = std::max(1, (G * NCH == 16 ? 768 : 512) / threads);
+    int64_t grid = std::min<int64_t>(warp_row ? (rows + 3) / 4 : rows, (int64_t)per_sm * sms);
+    if (NH >= 0 && !QUANT) grid = std::min<int64_t>(grid, kMaxAmaxPartials);
+    if (grid == 1) p.amax_out = amax;  // one CTA's maximum is the tensor's
+    if (n_partials != nullptr) *n_partials = (int)grid;
     const cudaError_t e =
-        p.C <= kNormWarpRowC
-            ? launch_pdl(rmsnorm_fwd_kernel<NH, QUANT, true>, dim3(grid), dim3(threads), 0, s, p)
-            : launch_pdl(rmsnorm_fwd_kernel<NH, QUANT, false>, dim3(grid), dim3(threads), 0, s, p);
+        warp_row ? launch_pdl(rmsnorm_fwd_kernel<NH, QUANT, 1, true>, dim3((unsigned)grid), dim3(threads), 0, s, p)
+                 : launch_pdl(rmsnorm_fwd_kernel<NH, QUANT, NCH, false>, dim3((unsigned)grid), dim3(threads), 0, s, p);
     count_launch();
     return e;
 }
 
 }  // namespace
 
-cudaError_t launch_rmsnorm_fwd(NormParams p, int nh, bool quant, float* amax, int sms, int* n_partials,
+cudaError_t launch_rmsnorm_fwd(const NormParams& p, int nh, bool quant, float* amax, int sms, int* n_partials,
                                cudaStream_t s) {
-    int threads = 0, grid = 0;
-    norm_grid(quant ? (p.R + 127) / 128 * 128 : p.R, p.C, sms, nh >= 0 && !quant ? kMaxAmaxPartials : 0, &threads, &grid);
-    if (grid == 1) p.amax_out = amax;  // one CTA's maximum is the tensor's
-    if (n_partials != nullptr) *n_partials = grid;
     if (quant) {
         switch (nh) {
-            case 0: return launch_norm_fwd_t<0, true>(p, threads, grid, s);
-            case 16: return launch_norm_fwd_t<16, true>(p, threads, grid, s);
-            default: return launch_norm_fwd_t<32, true>(p, threads, grid, s);
+            case 0: return launch_norm_fwd_t<0, true, 1>(p, amax, sms, n_partials, s);
+            case 16: return launch_norm_fwd_t<16, true, 1>(p, amax, sms, n_partials, s);
+            default: return launch_norm_fwd_t<32, true, 1>(p, amax, sms, n_partials, s);
+        }
+    }
+    if (nh == 32) return launch_norm_fwd_t<32, false, 1>(p, amax, sms, n_partials, s);
+    // at most 512 threads: two chunks of 16 each from 8192 columns on
+    if (p.C <= 8192) {
+        switch (nh) {
+            case -1: return launch_norm_fwd_t<-1, false, 1>(p, amax, sms, n_partials, s);
+            case 0: return launch_norm_fwd_t<0, false, 1>(p, amax, sms, n_partials, s);
+            default: return launch_norm_fwd_t<16, false, 1>(p, amax, sms, n_partials, s);
         }
     }
     switch (nh) {
-        case -1: return launch_norm_fwd_t<-1, false>(p, threads, grid, s);
-        case 0: return launch_norm_fwd_t<0, false>(p, threads, grid, s);
-        case 16: return launch_norm_fwd_t<16, false>(p, threads, grid, s);
-        default: return launch_norm_fwd_t<32, false>(p, threads, grid, s);
+        case -1: return launch_norm_fwd_t<-1, false, 2>(p, amax, sms, n_partials, s);
+        case 0: return launch_norm_fwd_t<0, false, 2>(p, amax, sms, n_partials, s);
+        default: return launch_norm_fwd_t<16, false, 2>(p, amax, sms, n_partials, s);
     }
 }
 
@@ -447,25 +523,18 @@ int64_t norm_bwd_partial_rows(int64_t R) { return std::min<int64_t>((R + 3) / 4 
 cudaError_t launch_rmsnorm_bwd(NormBwdParams p, float* dw, int accumulate, int sms, cudaStream_t s) {
     cudaError_t e;
     int owners;
-    if (p.C <= 512) {
+    if (p.C <= kNormWarpRowC) {
         const int grid = (int)std::min<int64_t>((p.R + 3) / 4, std::min(4 * sms, kMaxNormPartials / 4));
         owners = 4 * grid;
         auto run = [&](auto* kern) { return launch_pdl(kern, dim3(grid), dim3(128), 0, s, p); };
-        e = p.C <= 256 ? run(rmsnorm_bwd_warp_kernel<1>)
-                       : run(rmsnorm_bwd_warp_kernel<2>);
+        e = p.C <= 256 ? run(rmsnorm_bwd_warp_kernel<1>) : run(rmsnorm_bwd_warp_kernel<2>);
     } else {
-        // 512 threads per SM, and its shared memory shared out among their rings
-        const int threads = (int)((p.C + 511) / 512 * 32);
-        const int per_sm = std::max(1, 512 / threads);
+        const int threads = (int)((p.C + 511) / 512 * 32), per_sm = std::max(1, 512 / threads);
         const int stage = (p.dh != nullptr ? 3 : 2) * (int)p.C * 2;
-        p.stages = std::min(kNormMaxStages, kNormRingBytes / per_sm / stage);
+        p.stages = norm_stages(per_sm, stage);
         owners = (int)std::min<int64_t>(p.R, std::min(per_sm * sms, kMaxNormPartials));
-        auto run = [&](auto* kern) {
-            const cudaError_t a = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRingBytes);
-            if (a != cudaSuccess) return a;
-            return launch_pdl(kern, dim3(owners), dim3(threads), (size_t)(p.stages * stage), s, p);
-        };
-        e = threads <= 512 ? run(rmsnorm_bwd_ring_kernel<2, 512>) : run(rmsnorm_bwd_ring_kernel<2, 1024>);
+        e = threads <= 512 ? launch_norm_ring(rmsnorm_bwd_ring_kernel<2, 512>, owners, threads, p.stages * stage, p, s)
+                           : launch_norm_ring(rmsnorm_bwd_ring_kernel<2, 1024>, owners, threads, p.stages * stage, p, s);
     }
     count_launch();
     if (e != cudaSuccess) return e;

@@ -1203,6 +1203,10 @@ int norm_fwd_args(const void* x, int64_t ldx, const void* res, int64_t ldres, co
     p->ldh = ldh; p->ldy = ldy;
     p->rstd = rstd;
     p->signs = had_random(had) ? host_sign_bits(seed->rot, seed->rot_stream) : 0u;
+    const auto wide = [](const void* m, int64_t ld) {
+        return m == nullptr || (reinterpret_cast<uintptr_t>(m) % 32 == 0 && ld % 16 == 0);
+    };
+    p->wide = wide(x, ldx) && wide(res, ldres) && wide(h, ldh) && wide(y, ldy) && wide(w, 0);
     return QFP4_OK;
 }
 

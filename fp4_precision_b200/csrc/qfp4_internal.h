@@ -160,6 +160,7 @@ struct NormParams {
     float* q_tensor_scale;
     int64_t q_kb4;
     uint32_t q_round_up;
+    int wide;  // every matrix and w 32-byte aligned, strides multiples of 16
 };
 struct NormBwdParams {
     const uint16_t* dy;
@@ -179,7 +180,7 @@ constexpr int kMaxNormPartials = 592;
 // nh: -1 no amax, else the Hadamard size of the amax or of the quantization;
 // *n_partials receives the number of partial maxima; a single one goes to
 // *amax instead of p.amax_out.
-cudaError_t launch_rmsnorm_fwd(NormParams p, int nh, bool quant, float* amax, int sms, int* n_partials,
+cudaError_t launch_rmsnorm_fwd(const NormParams& p, int nh, bool quant, float* amax, int sms, int* n_partials,
                                cudaStream_t s);
 int64_t norm_bwd_partial_rows(int64_t R);
 cudaError_t launch_rmsnorm_bwd(NormBwdParams p, float* dw, int accumulate, int sms, cudaStream_t s);
