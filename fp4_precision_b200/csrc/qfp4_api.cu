@@ -1191,6 +1191,7 @@ int norm_fwd_args(const void* x, int64_t ldx, const void* res, int64_t ldres, co
     if (res != nullptr && (rc = check_matrix(res, R, C, ldres))) return rc;
     if ((res != nullptr || h != nullptr) && (rc = check_matrix(h, R, C, ldh))) return rc;
     if (y != nullptr && (rc = check_matrix(y, R, C, ldy))) return rc;
+    if (y != nullptr && y == h) return QFP4_ERR_INVALID_ARG;  // two outputs in one place
     if (R > 0 && rstd == nullptr) return QFP4_ERR_INVALID_ARG;
     p->x = static_cast<const uint16_t*>(x);
     p->res = static_cast<const uint16_t*>(res);

@@ -445,6 +445,14 @@ def _vector(t: torch.Tensor, n: int, dtype, i: int) -> int:
     return t.data_ptr()
 
 
+def _new_qtensor(like: torch.Tensor, fmt: int, rows: int, k: int) -> QTensor:
+    """empty_qtensor on like's device."""
+    codes = like.new_empty((rows, k // 2), dtype=torch.uint8)
+    scales = like.new_empty((max(scales_bytes(fmt, rows, k), 16),), dtype=torch.uint8)
+    ts = like.new_empty((1,), dtype=torch.float32)
+    return QTensor(codes, scales, ts, TensorDesc(codes.data_ptr(), scales.data_ptr(), ts.data_ptr()))
+
+
 def _ref(seed: Seed | None):
     return None if seed is None else ctypes.byref(seed)
 
@@ -474,8 +482,8 @@ def rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, eps: float, res: torch.Tensor 
                 seed: Seed | None = None, want_amax: bool = False, y=None, h=None, rstd=None, y_amax=None,
                 workspace=None):
     """h = x + res, y = h / rms(h) * w; see qfp4_rmsnorm_fwd. Returns (y, h,
-    rstd, y_amax): without res, h is x itself unless a buffer for it is given;
-    y_amax, y's NVFP4 tensor amax after the rotation `had`, is None unless
+    rstd, y_amax): without res, h is x itself unless a buffer for it is given
+    (which the backward pass needs if y goes to x's place); y_amax, y's NVFP4 tensor amax after the rotation `had`, is None unless
     wanted (want_amax or a buffer for it)."""
     shape, i = x.shape, _gpu(x)
     ldx = _matrix(x, shape, i)
@@ -515,7 +523,7 @@ def rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, eps: float, res: torch.Te
         y = torch.empty_like(x)
     h, hp, ldh, rp, ldr = _residual(x, res, h, shape, i)
     rstd = x.new_empty((R,), dtype=torch.float32) if rstd is None else rstd
-    out = empty_qtensor(MXFP4, R, C, x.device) if out is None else out
+    out = _new_qtensor(x, MXFP4, R, C) if out is None else out
     _go(lib().qfp4_rmsnorm_quantize, "qfp4_rmsnorm_quantize", i, x.data_ptr(), ldx, rp, ldr,
         _vector(w, C, torch.bfloat16, i), R, C, eps, hp, ldh, None if y is None else y.data_ptr(),
         0 if y is None else _matrix(y, shape, i), _vector(rstd, R, torch.float32, i), fmt, had, _ref(seed),
@@ -570,7 +578,7 @@ def quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, fmt: int, rounding:
     E = _groups(offsets, i)
     if out is None:
         Tp = max(group_rows(T, E), 0)
-        out = empty_qtensor(fmt, *((Tp, C) if axis == ROW else (C, Tp)), x.device)
+        out = _new_qtensor(x, fmt, *((Tp, C) if axis == ROW else (C, Tp)))
     wsp, wsb = None, 0
     if amax_in is None and fmt == NVFP4:
         wsp, wsb, workspace = _workspace(workspace, 4 * _WS_FLOATS, x)
@@ -709,12 +717,16 @@ class RmsNorm(torch.autograd.Function):
         y, h, rstd, _ = rmsnorm_fwd(x2, w, eps, res=r2, h=None if res is not None else torch.empty_like(x2))
         ctx.save_for_backward(h, w, rstd)
         ctx.has_res = res is not None
+        ctx.set_materialize_grads(False)  # an output that nothing uses has no gradient
         return y.view(x.shape), h.view(x.shape)
 
     @staticmethod
     def backward(ctx, dy, dh):
         h, w, rstd = ctx.saved_tensors
-        dx, dw = rmsnorm_bwd(dy.reshape(h.shape).contiguous(), h, w, rstd, dh=dh.reshape(h.shape).contiguous())
+        if dy is None:  # h alone was used: it is x + res
+            return dh, dh if ctx.has_res else None, None, None
+        dx, dw = rmsnorm_bwd(dy.reshape(h.shape).contiguous(), h, w, rstd,
+                             dh=None if dh is None else dh.reshape(h.shape).contiguous())
         dx = dx.view(dy.shape)
         return dx, dx if ctx.has_res else None, dw.to(w.dtype), None
 

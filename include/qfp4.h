@@ -400,8 +400,9 @@ int qfp4_linear_fwd_noalloc(const void* X, const void* W, void* Y, int64_t M, in
  * Requirements: C a multiple of 16 (32 with a 32-point Hadamard and for the
  *   quantization), 16 <= C <= QFP4_RMSNORM_MAX_COLS; 0 <= R < 2^31; eps >= 0
  *   and finite; strides >= C and multiples of 8; matrices, w and the workspace
- *   16-byte aligned; h required with res. h may be x or res, y may be x, dx may
- *   be dy or dh (same pointer and stride); no other overlap.
+ *   16-byte aligned (32-byte aligned rows are read and written faster); h
+ *   required with res. h may be x or res, y may be x, dx may be dy or dh (same
+ *   pointer and stride); no other overlap.
  * The pages have no counterpart: the norm is what feeds the layers they train. */
 #define QFP4_RMSNORM_MAX_COLS 16384
 int qfp4_rmsnorm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* w, int64_t R, int64_t C,

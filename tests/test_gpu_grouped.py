@@ -128,6 +128,56 @@ def test_gemm_is_the_product_of_each_group(name, fmt, form, dtype):
     assert torch.all(out[outside] == -5)
 
 
+@pytest.mark.parametrize("pair", ["0", "1"])
+@pytest.mark.parametrize("name", ["ragged", "skewed", "outside", "none"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_both_gemm_kernels_give_the_same(monkeypatch, pair, name, dtype):
+    """The CTA-pair and the single-CTA kernel, whichever the group sizes choose."""
+    sizes, off, T, offsets = split(name)
+    E, N, K = len(sizes), 384, 320
+    xp = padded(cpu((T, K), 51), sizes, off, T).cuda()
+    A = Q.quantize(xp, Q.NVFP4, Q.RTN, Q.HAD_NONE, Q.ROW)
+    B = Q.quantize(cpu((E * N, K), 52).cuda(), Q.NVFP4, Q.RTN, Q.HAD_NONE, Q.ROW)
+    want = Q.gemm_grouped(A, B, offsets, T, out=torch.zeros((T, N), dtype=torch.float32, device="cuda"))
+    monkeypatch.setenv("QFP4_GEMM_PAIR", pair)
+    got = Q.gemm_grouped(A, B, offsets, T, out=torch.zeros((T, N), dtype=dtype, device="cuda"))
+    Q.status()
+    assert torch.all((got.float() - want).abs() <= (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -20) * want.abs()
+                     + 2.0 ** -20 * want.norm(dim=1, keepdim=True))
+
+
+@pytest.mark.parametrize("pair", ["0", "1"])
+@pytest.mark.parametrize("T,N,K", [(1, 8, 64), (200, 72, 192), (129, 264, 64), (300, 1000, 448)])
+@pytest.mark.parametrize("fmt", [Q.NVFP4, Q.MXFP4])
+def test_gemm_of_one_group_with_odd_sizes(monkeypatch, pair, T, N, K, fmt):
+    """One group: N a multiple of 8, K of 64."""
+    monkeypatch.setenv("QFP4_GEMM_PAIR", pair)
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    x, w = cpu((T, K), 53), cpu((N, K), 54)
+    xp = padded(x, [T], [0, T], T)
+    (A, B), (a, b) = operands(fmt, Q.HAD_NONE, xp, Q.ROW, w, Q.ROW)
+    for dtype in (torch.bfloat16, torch.float32):
+        out, guard = helpers.guarded_matrix(T, N, dtype, "cuda")
+        Q.gemm_grouped(A, B, off, T, out=out)
+        Q.status()
+        helpers.assert_guards_intact(guard)
+        within(out, a[:T] @ b.T, O.GEMM_REL_BOUND * (np.abs(a[:T]) @ np.abs(b).T), dtype == torch.bfloat16)
+
+
+@pytest.mark.parametrize("C", [8, 40, 200, 1032])
+@pytest.mark.parametrize("had", [Q.HAD_NONE, Q.HAD_DET16, Q.HAD_DET32])
+def test_quantize_along_tokens_with_odd_widths(C, had):
+    sizes, off, T, offsets = split("ragged")
+    x = cpu((T, C), 55)
+    for fmt in (Q.NVFP4, Q.MXFP4):
+        q = Q.quantize_grouped(x.cuda(), offsets, fmt, Q.RTN, had, Q.COL)
+        want = O.quantize(padded(x, sizes, off, T), fmt, O.RTN, had, O.COL)
+        assert np.array_equal(helpers.to_numpy_u8(q.codes), want.codes)
+        flat = helpers.to_numpy_u8(q.scales)
+        assert np.array_equal(helpers.unswizzle_scales(flat, C, q.k, Q.BLOCK[fmt]), want.scales)
+    Q.status()
+
+
 @pytest.mark.parametrize("name", SPLITS)
 @pytest.mark.parametrize("fmt", [Q.NVFP4, Q.MXFP4])
 @pytest.mark.parametrize("kind", ["f32", "bf16", "add"])

@@ -283,6 +283,10 @@ def test_before_an_fp4_layer():
     yy.backward(dy)
     _, h1, r1, _ = Q.rmsnorm_fwd(x, w, EPS)
     assert same(a.grad, Q.rmsnorm_bwd(dy, h1, w, r1)[0])
+    b, c = x.clone().requires_grad_(), res.clone().requires_grad_()
+    _, hh = Q.RmsNorm.apply(b, c, w, EPS)       # and through h alone
+    hh.backward(dh)
+    assert same(b.grad, dh) and same(c.grad, dh)
     Q.status()
 
 

@@ -37,6 +37,7 @@ def norm_fwd(lib, **kw):
     (dict(x=None), Q.ERR_INVALID_ARG), (dict(w=None), Q.ERR_INVALID_ARG), (dict(w=ODD), Q.ERR_MISALIGNED),
     (dict(y=None), Q.ERR_INVALID_ARG), (dict(ldy=56), Q.ERR_INVALID_ARG), (dict(rstd=None), Q.ERR_INVALID_ARG),
     (dict(res=P, ldres=64), Q.ERR_INVALID_ARG), (dict(res=P, ldres=64, h=ODD, ldh=64), Q.ERR_MISALIGNED),
+    (dict(h=P, ldh=64), Q.ERR_INVALID_ARG),  # y's place
     (dict(eps=-1.0), Q.ERR_INVALID_ARG), (dict(eps=float("nan")), Q.ERR_INVALID_ARG),
     (dict(eps=float("inf")), Q.ERR_INVALID_ARG),
     (dict(had=5), Q.ERR_INVALID_ARG), (dict(had=-1), Q.ERR_INVALID_ARG),
