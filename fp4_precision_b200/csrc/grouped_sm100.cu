@@ -220,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     if (warp == 0) tmem_alloc_pair(tmem_slot, TMEM_COLS);
     pdl_wait();  // the offsets and the operands are written (and the previous readers of D done)
     pdl_launch_dependents();
-    if (warp == 1) build_groups(groups, p.offsets, p.E, p.T, 2 * BM, lane);
+    if (warp == 1) build_groups(groups, p.offsets, 1, p.E, p.T, 2 * BM, lane);
     tc_fence_before();
     __syncwarp();
     cluster_sync();  // barriers of both CTAs initialised, tensor memory allocated, groups known
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (warp == 0) tmem_alloc(tmem_slot, TMEM_COLS);
     pdl_wait();  // the offsets and the operands are written (and the previous readers of D done)
     pdl_launch_dependents();
-    if (warp == 1) build_groups(groups, p.offsets, p.E, p.T, BM, lane);
+    if (warp == 1) build_groups(groups, p.offsets, 1, p.E, p.T, BM, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -199,10 +199,17 @@ struct Groups {
     int32_t E;
     int64_t T;
 };
+// Rows of the padded layout: what T rows in E groups, at most min(E, T) of them
+// not empty, can need. A multiple of 128.
+int64_t group_rows(int64_t T, int32_t E) {
+    return T <= 0 ? 0 : (T + 127 * std::min<int64_t>(E, T)) / 128 * 128;
+}
+
 void set_groups(QuantParams& p, const Groups* gr) {
     if (gr == nullptr) return;
     p.group_offsets = gr->offsets;
     p.groups = gr->E;
+    p.group_step = 1;
     p.group_T = (int)gr->T;
 }
 
@@ -393,6 +400,12 @@ int run_amax(const void* x, int64_t R, int64_t C, int64_t ld, int32_t had, int32
     p.x = static_cast<const uint16_t*>(x);
     p.R = R; p.C = C; p.ld = ld;
     p.rows = g.rows; p.k = g.k;
+    if (gr != nullptr && axis == QFP4_AXIS_ROW) {
+        // along the rows only the rows matter: all groups as one, without their padding
+        p.groups = 1;
+        p.group_step = gr->E;
+        p.R = p.rows = group_rows(gr->T, 1);
+    }
     p.signs = signs;
     p.amax_out = partials;
     const int nh = had_n(had);
@@ -400,7 +413,7 @@ int run_amax(const void* x, int64_t R, int64_t C, int64_t ld, int32_t had, int32
     CUtensorMap tm[2];
     int rc = gr ? make_group_tmaps(tm, x, gr->T, C, ld, axis, G) : make_input_tmap(tm, x, R, C, ld, axis, G);
     if (rc) return rc;
-    *n_partials = amax_partial_count(sms, quant_tiles(axis, g.rows, g.k, G));
+    *n_partials = amax_partial_count(sms, quant_tiles(axis, p.rows, p.k, G));
     cudaError_t e = launch_amax(p, axis, nh, tm, *n_partials, s);
     return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
 }
@@ -1217,12 +1230,6 @@ int set_zero(float* v, int64_t n, cudaStream_t s) {
 }
 
 // ---- groups of rows -------------------------------------------------------------
-// Rows of the padded layout: what T rows in E groups, at most min(E, T) of them
-// not empty, can need. A multiple of 128.
-int64_t group_rows(int64_t T, int32_t E) {
-    return T <= 0 ? 0 : (T + 127 * std::min<int64_t>(E, T)) / 128 * 128;
-}
-
 int check_groups(const int32_t* offsets, int32_t E, int64_t T) {
     if (E < 1 || E > QFP4_MAX_GROUPS || T < 0 || T > 0x7fffffffLL) return QFP4_ERR_INVALID_ARG;
     if (group_rows(T, E) > 0x7fffffffLL || offsets == nullptr) return QFP4_ERR_INVALID_ARG;

@@ -59,7 +59,7 @@ struct QuantParams {
     // groups, and R (and so rows or k) counts those of the padded layout; tmap
     // points to two maps (GroupMaps in quant.cu).
     const int* group_offsets;
-    int groups, group_T;
+    int groups, group_step, group_T;  // offsets of the groups: every group_step-th
 };
 
 // Launchers (quant.cu). Return cudaSuccess or the launch error.

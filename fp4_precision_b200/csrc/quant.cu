@@ -823,7 +823,7 @@ __device__ __forceinline__ void load_group_tiles(const GroupMaps& maps, const Qu
     static_assert(SEGS == 1 || BOXES == 1, "one of the two");
     constexpr bool kRow = std::is_same_v<Order, RowOrder>;
     GroupSmem<STAGES>& gs = *reinterpret_cast<GroupSmem<STAGES>*>(tiles + STAGES * STAGE_BYTES);
-    build_groups(gs.table, p.group_offsets, p.groups, p.group_T, 128, lane);
+    build_groups(gs.table, p.group_offsets, p.group_step, p.groups, p.group_T, 128, lane);
     __syncwarp();
     int i = 0;
     for (TileWalk<STAGES> w(tiles_c); w.tr < tiles_r; w.next(), ++i) {
