@@ -240,6 +240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                 const int brow = (WGRAD ? 0 : w.e * p.b_rows) + w.n0;
                 const int bk0 = WGRAD ? w.k0 : w.e * p.b_k;
                 const int kt_n = (w.k + BK - 1) / BK;
+                const bool b_half = w.n0 + 128 >= p.N;  // columns of the second CTA's B rows are not stored
                 for (int kt = 0; kt < kt_n; ++kt, ++it) {
                     const int s = it % P_STAGES;
                     if (it >= P_STAGES && !mbar_wait_cluster(&empty[s], ((it / P_STAGES) + 1) & 1)) {
@@ -250,9 +251,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                     tma_load_3d(sSFA + s * P_SFA, &tmSFA, &sf_load[s], 0, w.k0 / SF_K + kt * ATOMS_PER_KT, arow / 128);
                     tma_load_3d(sSFB + s * P_SFB, &tmSFB, &sf_load[s], 0, bk0 / SF_K + kt * ATOMS_PER_KT, brow / 128);
                     const uint32_t bar_leader = mapa_shared(smem_u32(&full[s]), 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], AB_TX);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], b_half ? AB_TX - P_B : AB_TX);
                     tma_load_2d_pair(sA + s * P_A, &tmA, bar_leader, w.k0 / 2 + kt * (BK / 2), arow);
-                    tma_load_2d_pair(sB + s * P_B, &tmB, bar_leader, bk0 / 2 + kt * (BK / 2), brow + (int)rank * 128);
+                    if (rank == 0 || !b_half)
+                        tma_load_2d_pair(sB + s * P_B, &tmB, bar_leader, bk0 / 2 + kt * (BK / 2), brow + (int)rank * 128);
                 }
             }
             drain_loads(rank == 0 ? full : nullptr, sf_load, P_STAGES, it);
@@ -353,7 +355,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 
 // Few rows per group (the rows product alone): single CTAs on 128 x 256 tiles,
 // as the dense single-CTA kernel. A pair's second CTA would multiply rows that
-// are no group's, and there would be half as many tiles in flight.
+// are no group's, and there would be half as many tiles in flight. Bound by the
+// weights' arrival (488 rows of 64 groups, 1408 x 2048: 107 MB in 23.9 us, of
+// which about 5 are the start and the end; pairs 30.0, tiles of 128 x 128 25.3).
 constexpr int GS_SMEM = SMEM_BYTES + (int)sizeof(GroupTable);
 static_assert(GS_SMEM <= 227 * 1024, "shared memory of one CTA");
 
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
                 const GroupTile w = walk.at(p, t);
                 const int arow = groups.padded[w.e] + w.m0, brow = w.e * p.b_rows + w.n0, bk0 = w.e * p.b_k;
-                const int nrb = (w.n0 + 128 < p.N) ? 2 : 1;  // B row blocks of this group
+                const int nrb = w.n0 + 128 < p.N ? 2 : 1;  // B row blocks of this group
                 for (int kt = 0; kt < KT; ++kt, ++it) {
                     const int s = it % STAGES;
                     if (it >= STAGES && !mbar_wait(&empty[s], ((it / STAGES) + 1) & 1)) {
@@ -431,9 +435,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         bulk_load(sSFB + s * SFB_STAGE + rb * (ATOMS_PER_KT * 512),
                                   p.sfb + ((int64_t)(brow / 128 + rb) * p.atoms_b + bk0 / SF_K + katom) * 512, atoms * 512,
                                   &sf_load[s]);
-                    mbar_arrive_expect_tx(&full[s], A_STAGE + B_STAGE);
+                    mbar_arrive_expect_tx(&full[s], A_STAGE + nrb * P_B);
                     tma_load_2d(sA + s * A_STAGE, &tmA, &full[s], kt * (BK / 2), arow);
-                    tma_load_2d(sB + s * B_STAGE, &tmB, &full[s], bk0 / 2 + kt * (BK / 2), brow);
+                    for (int rb = 0; rb < nrb; ++rb)
+                        tma_load_2d(sB + s * B_STAGE + rb * P_B, &tmB, &full[s], bk0 / 2 + kt * (BK / 2), brow + 128 * rb);
                 }
             }
             drain_loads(full, sf_load, STAGES, it);

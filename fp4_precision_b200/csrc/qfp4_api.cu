@@ -1264,12 +1264,15 @@ int run_grouped(const qfp4_tensor* A, const qfp4_tensor* B, bool wgrad, int64_t 
     p.sfb = B->scales;
     p.atoms_a = (int)atoms_k(A->k);
     p.atoms_b = (int)atoms_k(B->k);
-    // as the dense GEMM: pairs unless the groups have at most 128 rows, here on average
-    const bool pair = wgrad || use_pair_gemm(p.T / p.E);
+    // As the dense GEMM, whose pairs begin where A has more rows than one CTA's
+    // tile: here above 96 rows per group on average. 64 rows (32 groups, 2048 x
+    // 2048): pairs 22.6 us, single CTAs 19.2; 125 rows: 23.7 and 25.1; 64 groups
+    // of 125 rows, 1408 x 2048: 34.3 and 36.9.
+    const bool pair = wgrad || use_pair_gemm(p.T > 96 * (int64_t)p.E ? kGemmBM + 1 : kGemmBM);
     CUtensorMap tA, tB, tSFA, tSFB, tD;
     int rc;
     if ((rc = make_codes_tmap(&tA, A->codes, A->rows, A->k, kGemmBM))) return rc;
-    if ((rc = make_codes_tmap(&tB, B->codes, B->rows, B->k, pair ? 128 : kGemmBN))) return rc;
+    if ((rc = make_codes_tmap(&tB, B->codes, B->rows, B->k, 128))) return rc;
     if ((rc = make_scale_tmap(&tSFA, A->scales, A->rows, atoms_k(A->k), apk, 1))) return rc;
     if ((rc = make_scale_tmap(&tSFB, B->scales, B->rows, atoms_k(B->k), apk, 2))) return rc;
     if ((rc = make_out_tmap(&tD, p.D, d_rows, p.N, p.ldd, p.out_f32))) return rc;

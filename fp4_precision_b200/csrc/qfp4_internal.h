@@ -208,8 +208,8 @@ struct GroupedParams {
     int atoms_a, atoms_b;
 };
 // wgrad: the reduction runs over the groups' rows (D [E M x N]); else over K,
-// with the groups along the rows of A and D, and by single CTAs with pair =
-// false (tmapB then has boxes of 256 rows; the last three maps are not read).
+// with the groups along the rows of A and D, by CTA pairs or (which do not read
+// the last three maps) single CTAs.
 cudaError_t launch_gemm_grouped(const GroupedParams& p, int fmt, bool wgrad, bool pair, const CUtensorMap* tmapA,
                                 const CUtensorMap* tmapB, const CUtensorMap* tmapSFA, const CUtensorMap* tmapSFB,
                                 const CUtensorMap* tmapD, cudaStream_t s, int sms);
