@@ -478,7 +478,7 @@ cudaError_t launch_norm_fwd_t(NormParams p, float* amax, int sms, int* n_partial
     constexpr int G = kNormChunk<NH, QUANT>;
     const int64_t rows = QUANT ? (p.R + 127) / 128 * 128 : p.R;
     const bool warp_row = p.C <= 32 * G;
-    const int threads = warp_row ? 128 : (int)((p.C / (G * NCH) + 31) / 32 * 32);
+    const int threads = warp_row ? 128 : (int)((p.C + G * NCH * 32 - 1) / (G * NCH * 32) * 32);
     const int per_sm = std::max(1, (G * NCH == 16 ? 768 : 512) / threads);
     int64_t grid = std::min<int64_t>(warp_row ? (rows + 3) / 4 : rows, (int64_t)per_sm * sms);
     if (NH >= 0 && !QUANT) grid = std::min<int64_t>(grid, kMaxAmaxPartials);

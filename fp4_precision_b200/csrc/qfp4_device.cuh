@@ -29,7 +29,7 @@ __device__ __forceinline__ void raise_device_error(uint32_t code) { atomicOr(&g_
 // DEV_ERR_BOUNDS and returns a scratch sink instead, so nothing outside the
 // buffer is written and nothing traps (qfp4_status then returns
 // QFP4_ERR_BOUNDS). In the normal build chk() returns p.
-__device__ __align__(16) uint8_t g_bounds_sink[64];
+__device__ __align__(32) uint8_t g_bounds_sink[64];
 template <typename T>
 __device__ __forceinline__ T* chk(T* p, const void* base, int64_t size, int64_t n = (int64_t)sizeof(T)) {
 #ifdef QFP4_BOUNDS_CHECK
