@@ -1273,9 +1273,11 @@ int run_grouped(const qfp4_tensor* A, const qfp4_tensor* B, bool wgrad, int64_t 
     int rc;
     if ((rc = make_codes_tmap(&tA, A->codes, A->rows, A->k, kGemmBM))) return rc;
     if ((rc = make_codes_tmap(&tB, B->codes, B->rows, B->k, 128))) return rc;
-    if ((rc = make_scale_tmap(&tSFA, A->scales, A->rows, atoms_k(A->k), apk, 1))) return rc;
-    if ((rc = make_scale_tmap(&tSFB, B->scales, B->rows, atoms_k(B->k), apk, 2))) return rc;
-    if ((rc = make_out_tmap(&tD, p.D, d_rows, p.N, p.ldd, p.out_f32))) return rc;
+    if (pair) {
+        if ((rc = make_scale_tmap(&tSFA, A->scales, A->rows, atoms_k(A->k), apk, 1))) return rc;
+        if ((rc = make_scale_tmap(&tSFB, B->scales, B->rows, atoms_k(B->k), apk, 2))) return rc;
+        if ((rc = make_out_tmap(&tD, p.D, d_rows, p.N, p.ldd, p.out_f32))) return rc;
+    }
     const cudaError_t e = launch_gemm_grouped(p, A->fmt, wgrad, pair, &tA, &tB, &tSFA, &tSFB, &tD, s, sms);
     return e == cudaSuccess ? QFP4_OK : cuda_fail(e);
 }
