@@ -151,7 +151,8 @@ def _check(status: int, what: str):
 
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        torch.cuda.init()
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -406,8 +407,12 @@ _WS_FLOATS = 1024  # the quantizers' workspace as fp32 words
 
 
 def _on_stream(f):
+    """Adds a keyword `stream`, on which the call then runs."""
     @functools.wraps(f)
-    def call(*args, stream=None, **kwargs):
+    def call(*args, **kwargs):
+        if "stream" not in kwargs:
+            return f(*args, **kwargs)
+        stream = kwargs.pop("stream")
         if stream is None:
             return f(*args, **kwargs)
         with torch.cuda.stream(stream):
@@ -435,13 +440,16 @@ def _gpu(t: torch.Tensor) -> int:
 
 def _matrix(t: torch.Tensor, shape, i: int, dtype=torch.bfloat16) -> int:
     """Check a matrix with contiguous rows on GPU i; its row stride (a single row's is not looked at)."""
-    assert t.dtype is dtype and t.shape == shape and t.get_device() == i and (t.stride(1) == 1 or shape[1] <= 1)
+    assert t.dtype is dtype and t.shape == shape and t.get_device() == i
+    if t.is_contiguous():
+        return shape[1] or 8
+    assert t.stride(1) == 1 or shape[1] == 1
     return t.stride(0) if shape[0] > 1 else max(shape[1], 8)
 
 
 def _vector(t: torch.Tensor, n: int, dtype, i: int) -> int:
     """Check a contiguous vector of n on GPU i; its address."""
-    assert t.dtype is dtype and t.shape == (n,) and (n <= 1 or t.stride(0) == 1) and t.get_device() == i
+    assert t.dtype is dtype and t.shape == (n,) and t.is_contiguous() and t.get_device() == i
     return t.data_ptr()
 
 
@@ -495,7 +503,8 @@ def rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, eps: float, res: torch.Tensor 
     if amax and rstd is None and y_amax is None and workspace is None:
         # one allocation for the three
         workspace = x.new_empty((_WS_FLOATS + 4 + R,), dtype=torch.float32)
-        y_amax, rstd = workspace[_WS_FLOATS:_WS_FLOATS + 1], workspace[_WS_FLOATS + 4:]
+        y_amax = workspace.as_strided((1,), (1,), _WS_FLOATS)
+        rstd = workspace.as_strided((R,), (1,), _WS_FLOATS + 4)
         wsp, wsb = workspace.data_ptr(), 4 * _WS_FLOATS
         ap, rsp = wsp + 4 * _WS_FLOATS, wsp + 4 * (_WS_FLOATS + 4)
     else:
