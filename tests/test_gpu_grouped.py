@@ -405,3 +405,49 @@ def test_larger_and_smallest(T, E, N, K):
             tol = 2.0 ** -8 * want.abs() + 2.0 ** -16 * want.norm(dim=1, keepdim=True)
             assert torch.all((Y[r].float() - want).abs() <= tol)
     Q.status()
+
+
+def test_offsets_past_32_bits():
+    """Inputs and outputs of more than 2^31 elements: their last rows, columns and groups against the dense calls."""
+    T, C = 140_000, 16384
+    cut = 69_999
+    off = torch.tensor([0, cut, T], dtype=torch.int32, device="cuda")
+    x = torch.zeros((T, C), dtype=torch.bfloat16, device="cuda")
+    x[-200:] = cpu((200, C), 61).cuda()
+    amax = torch.full((1,), 6.0, device="cuda")
+    p = (cut + 127) // 128 * 128
+    q = Q.quantize_grouped(x, off, Q.NVFP4, Q.SR, Q.HAD_DET16, Q.ROW, amax_in=amax)
+    q0 = Q.quantize(torch.cat((torch.zeros((p, C), dtype=torch.bfloat16, device="cuda"), x[cut:])), Q.NVFP4, Q.SR,
+                    Q.HAD_DET16, Q.ROW, amax_in=amax)
+    assert torch.equal(q.codes[p:p + T - cut], q0.codes[p:]) and not q.codes[:p].any()
+    del q, q0
+    q = Q.quantize_grouped(x, off, Q.MXFP4, Q.RTN, Q.HAD_DET32, Q.COL)
+    first = (T - cut) // 128 * 128 - 128  # of the second group's rows: its last whole segment and the rest
+    rest = T - cut - first
+    want = Q.quantize_grouped(x[cut + first:], torch.tensor([0, rest], dtype=torch.int32, device="cuda"), Q.MXFP4, Q.RTN,
+                              Q.HAD_DET32, Q.COL)
+    k0, n = p + first, (rest + 127) // 128 * 128
+    assert torch.equal(q.codes[:, k0 // 2:(k0 + n) // 2], want.codes[:, :n // 2]) and want.codes.any()
+    assert not q.codes[:, :k0 // 2 - 64].any()
+    del q, want, x
+    # D of T x N
+    T, N, K = 70_000, 33_024, 128
+    off = torch.tensor([0, 65_000, T], dtype=torch.int32, device="cuda")
+    X, W = cpu((T, K), 62).cuda(), cpu((2 * N, K), 63).cuda()
+    A = Q.quantize_grouped(X, off, Q.MXFP4, Q.RTN, Q.HAD_NONE, Q.ROW)
+    B = Q.quantize(W, Q.MXFP4, Q.RTN, Q.HAD_NONE, Q.ROW)
+    Y = Q.gemm_grouped(A, B, off, T)
+    d = Q.gemm(Q.quantize(X[-300:].contiguous(), Q.MXFP4, Q.RTN, Q.HAD_NONE, Q.ROW),
+               Q.quantize(W[N:].contiguous(), Q.MXFP4, Q.RTN, Q.HAD_NONE, Q.ROW))
+    assert torch.equal(Y[-300:], d)
+    del Y, d, A, B
+    # dW of E x M x N
+    E, M, N, T = 8, 16384, 16640, 300
+    off = torch.tensor([0, 10, 20, 30, 40, 50, 60, 70, T], dtype=torch.int32, device="cuda")
+    dy, X = cpu((T, M), 64).cuda(), cpu((T, N), 65).cuda()
+    A, B = (Q.quantize_grouped(t, off, Q.MXFP4, Q.RTN, Q.HAD_DET32, Q.COL) for t in (dy, X))
+    dW = Q.gemm_grouped_wgrad(A, B, off, T)
+    o1 = torch.tensor([0, T - 70], dtype=torch.int32, device="cuda")
+    a, b = (Q.quantize_grouped(t[70:].contiguous(), o1, Q.MXFP4, Q.RTN, Q.HAD_DET32, Q.COL) for t in (dy, X))
+    assert torch.equal(dW[-1], Q.gemm_grouped_wgrad(a, b, o1, T - 70)[0])
+    Q.status()
