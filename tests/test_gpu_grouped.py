@@ -407,6 +407,36 @@ def test_larger_and_smallest(T, E, N, K):
     Q.status()
 
 
+def test_training_step_captured():
+    """norm -> experts, forward and backward through the autograd functions, captured and replayed on other data."""
+    T, E, N, K = 256, 3, 256, 512
+    off = torch.tensor([0, 100, 100, T], dtype=torch.int32, device="cuda")
+    x, r = (cpu((T, K), s).cuda().requires_grad_() for s in (71, 72))
+    w, W = torch.ones(K, dtype=torch.bfloat16, device="cuda").requires_grad_(), cpu((E, N, K), 73, 0.05).cuda().requires_grad_()
+    dY, dh = cpu((T, N), 74).cuda(), cpu((T, K), 75).cuda()
+    rec, seed = Q.recipe("QUARTET2_NVFP4"), Q.make_seed(1, 2)
+
+    def step():
+        y, h = Q.RmsNorm.apply(x, r, w, 1e-5)
+        return torch.autograd.grad((Q.Fp4GroupedLinear.apply(y, W, off, rec, seed), h), (x, r, w, W), (dY, dh))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for s in (76, 77):
+        with torch.no_grad():
+            x.copy_(cpu((T, K), s))
+        graph.replay()
+        held = [t.clone() for t in got]
+        assert all(torch.equal(a, b) for a, b in zip(held, step()))
+    Q.status()
+
+
 def test_offsets_past_32_bits():
     """Inputs and outputs of more than 2^31 elements: their last rows, columns and groups against the dense calls."""
     T, C = 140_000, 16384
