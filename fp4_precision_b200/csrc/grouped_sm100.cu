@@ -220,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     if (warp == 0) tmem_alloc_pair(tmem_slot, TMEM_COLS);
     pdl_wait();  // the offsets and the operands are written (and the previous readers of D done)
     pdl_launch_dependents();
-    if (warp == 1) build_groups(groups, p.offsets, 1, p.E, p.T, 2 * BM, lane);
+    if (warp == 1) build_groups(groups, p.offsets, p.E, p.T, 2 * BM, lane);
     tc_fence_before();
     __syncwarp();
     cluster_sync();  // barriers of both CTAs initialised, tensor memory allocated, groups known
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (warp == 0) tmem_alloc(tmem_slot, TMEM_COLS);
     pdl_wait();  // the offsets and the operands are written (and the previous readers of D done)
     pdl_launch_dependents();
-    if (warp == 1) build_groups(groups, p.offsets, 1, p.E, p.T, BM, lane);
+    if (warp == 1) build_groups(groups, p.offsets, p.E, p.T, BM, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -561,10 +561,11 @@ cudaError_t launch_gemm_grouped(const GroupedParams& p, int fmt, bool wgrad, boo
         auto run = [&](auto* kern) {
             const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GS_SMEM);
             if (e != cudaSuccess) return e;
-            return launch_pdl(kern, dim3((unsigned)std::min<int64_t>(sms, tiles)), dim3(kGemmThreads), GS_SMEM, s, *tmapA,
-                              *tmapB, p);
+            const dim3 grid((unsigned)std::min<int64_t>(sms, tiles));
+            return launch_pdl(kern, grid, dim3(kGemmThreads), GS_SMEM, s, *tmapA, *tmapB, p);
         };
-        const cudaError_t e = fmt == kNvfp4 ? run(gemm_grouped_single_kernel<kNvfp4>) : run(gemm_grouped_single_kernel<kMxfp4>);
+        const cudaError_t e =
+            fmt == kNvfp4 ? run(gemm_grouped_single_kernel<kNvfp4>) : run(gemm_grouped_single_kernel<kMxfp4>);
         count_launch();
         return e;
     }

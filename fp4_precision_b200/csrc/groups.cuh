@@ -16,17 +16,15 @@ struct GroupTable {
     __device__ __forceinline__ int size(int e) const { return row[e + 1] - row[e]; }
 };
 
-// Built by one warp from the device offsets, every step-th of them (step = 1:
-// the groups; step = the number of groups: all of them as one). All loads are issued before the
+// Built by one warp from the device offsets. All loads are issued before the
 // first use (one memory latency for 256 groups). Offsets that fall anywhere or
 // leave [0, T] would lead out of the buffers: they raise the device error word
 // and make every group empty.
-__device__ __forceinline__ void build_groups(GroupTable& g, const int* offsets, int step, int E, int T, int tile_rows,
-                                             int lane) {
+__device__ __forceinline__ void build_groups(GroupTable& g, const int* offsets, int E, int T, int tile_rows, int lane) {
     constexpr int STEPS = kMaxGroups / 32 + 1;
     int o[STEPS + 1];  // o[i]: offset 32 i + lane
 #pragma unroll
-    for (int i = 0; i <= STEPS; ++i) o[i] = 32 * i + lane <= E ? offsets[(32 * i + lane) * step] : 0;
+    for (int i = 0; i <= STEPS; ++i) o[i] = 32 * i + lane <= E ? offsets[32 * i + lane] : 0;
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {

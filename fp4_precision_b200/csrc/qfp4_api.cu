@@ -205,12 +205,16 @@ int64_t group_rows(int64_t T, int32_t E) {
     return T <= 0 ? 0 : (T + 127 * std::min<int64_t>(E, T)) / 128 * 128;
 }
 
-void set_groups(QuantParams& p, const Groups* gr) {
+// For a pass along the rows (axis) p's rows are x's.
+void set_groups(QuantParams& p, const Groups* gr, int axis) {
     if (gr == nullptr) return;
     p.group_offsets = gr->offsets;
     p.groups = gr->E;
-    p.group_step = 1;
     p.group_T = (int)gr->T;
+    if (axis == QFP4_AXIS_ROW) {
+        p.group_rows = group_rows(gr->T, gr->E);
+        p.R = p.rows = gr->T;
+    }
 }
 
 // The two TMA views of x (T x C) for a pass over rows in groups.
@@ -396,16 +400,10 @@ int run_amax(const void* x, int64_t R, int64_t C, int64_t ld, int32_t had, int32
              const Geometry& g, float* partials, int* n_partials, int sms, cudaStream_t s,
              const Groups* gr = nullptr) {
     QuantParams p{};
-    set_groups(p, gr);
     p.x = static_cast<const uint16_t*>(x);
     p.R = R; p.C = C; p.ld = ld;
     p.rows = g.rows; p.k = g.k;
-    if (gr != nullptr && axis == QFP4_AXIS_ROW) {
-        // along the rows only the rows matter: all groups as one, without their padding
-        p.groups = 1;
-        p.group_step = gr->E;
-        p.R = p.rows = group_rows(gr->T, 1);
-    }
+    set_groups(p, gr, axis);
     p.signs = signs;
     p.amax_out = partials;
     const int nh = had_n(had);
@@ -485,10 +483,10 @@ int quantize_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t fmt, 
     const uint32_t signs = had_random(had) ? host_sign_bits(seed->rot, seed->rot_stream) : 0u;
     const int nh = had_n(had);
     QuantParams p{};
-    set_groups(p, gr);
     p.x = static_cast<const uint16_t*>(x);
     p.R = R; p.C = C; p.ld = ld;
     p.rows = g.rows; p.k = g.k;
+    set_groups(p, gr, axis);
     p.codes = out->codes;
     p.scales = out->scales;
     p.tensor_scale = out->tensor_scale;
@@ -580,7 +578,7 @@ int quantize_dual_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t 
     fill_out(out_row, R, C, fmt, had_row, seed_row);
     fill_out(out_col, C, R, fmt, had_col, seed_col);
     QuantParams p{};
-    set_groups(p, gr);
+    set_groups(p, gr, QFP4_AXIS_COL);
     p.x = static_cast<const uint16_t*>(x);
     p.R = R; p.C = C; p.ld = ld;
     p.rows = C; p.k = R;  // the column orientation
@@ -849,7 +847,7 @@ int amax_rowcol_impl(const void* x, int64_t R, int64_t C, int64_t ld, int32_t ha
     // (rows in groups: sizes of 0 and 16 may differ)
     if (nh <= 16 && (gr != nullptr ? had_n(had_row) <= 16 : had_n(had_row) == nh)) {
         QuantParams p{};
-        set_groups(p, gr);
+        set_groups(p, gr, QFP4_AXIS_COL);
         p.x = static_cast<const uint16_t*>(x);
         p.R = R; p.C = C; p.ld = ld;
         p.rows = g_col.rows; p.k = g_col.k;

@@ -55,11 +55,13 @@ struct QuantParams {
     // arrival counter, zeroed before the launch; the partials go to amax_out
     // and are read back through amax_partials.
     uint32_t* grid_counter;
-    // Rows in groups (nullptr: none): x then has group_T rows in `groups`
-    // groups, and R (and so rows or k) counts those of the padded layout; tmap
-    // points to two maps (GroupMaps in quant.cu).
+    // Rows in groups (nullptr: none): x has group_T rows. Along the columns, R
+    // and k count those of the padded layout; along the rows, R and rows those
+    // of x, and the outputs have group_rows. tmap points to two maps (GroupMaps
+    // in quant.cu).
     const int* group_offsets;
-    int groups, group_step, group_T;  // offsets of the groups: every group_step-th
+    int groups, group_T;
+    int64_t group_rows;
 };
 
 // Launchers (quant.cu). Return cudaSuccess or the launch error.

@@ -402,9 +402,10 @@ struct Group {
 };
 
 // Extents of the output buffers (bytes), for the bounds-checked build.
-__device__ __forceinline__ int64_t codes_extent(const QuantParams& p) { return p.rows * (p.k / 2); }
+__device__ __forceinline__ int64_t out_rows(const QuantParams& p) { return p.group_rows > 0 ? p.group_rows : p.rows; }
+__device__ __forceinline__ int64_t codes_extent(const QuantParams& p) { return out_rows(p) * (p.k / 2); }
 __device__ __forceinline__ int64_t scales_extent(const QuantParams& p) {
-    return (p.rows + 127) / 128 * (p.kb4 / 4) * 512;
+    return (out_rows(p) + 127) / 128 * (p.kb4 / 4) * 512;
 }
 __device__ __forceinline__ int64_t codes_row_extent(const QuantParams& p) { return p.R * (p.C / 2); }
 __device__ __forceinline__ int64_t scales_row_extent(const QuantParams& p) {
@@ -773,10 +774,13 @@ __device__ __forceinline__ void ring_init(Ring<STAGES>& ring) {
 }
 
 // ---------------------------------------------------------------------------
-// Rows in groups: a tile holds rows of the padded layout in segments of 128 (or
-// of the tile's, if fewer), each within one group or no group's. The producer
-// loads a segment from the group's own rows, which start at any row of x: one
-// box of consecutive rows, the first row as a coordinate of its own (a map
+// Rows in groups. Along the rows of x (blocks along the columns) a tile holds
+// rows of x from the first group's first row on; each thread finds its row's
+// place in the padded layout, and rows that are no group's are not written.
+// Along its columns a tile holds rows of the padded layout in segments of 128
+// (or of the tile's, if fewer), each within one group or no group's. The
+// producer loads a segment from the group's own rows, which start at any row of
+// x: one box of consecutive rows, the first row as a coordinate of its own (a map
 // dimension of one row's stride that the box crosses nowhere). Rows behind the
 // group's end arrive as whatever follows them and are masked by the compute
 // warps, which know each segment's row count; a segment without rows is not
@@ -813,6 +817,7 @@ template <int STAGES>
 struct GroupSmem {
     GroupTable table;
     int rows[STAGES][2];
+    int span[STAGES][2];  // along the rows: the groups of the tile's first and last row
 };
 
 // The producer warp: tiles of SEGS segments of SEG_ROWS x (64 BOXES), a
@@ -823,7 +828,7 @@ __device__ __forceinline__ void load_group_tiles(const GroupMaps& maps, const Qu
     static_assert(SEGS == 1 || BOXES == 1, "one of the two");
     constexpr bool kRow = std::is_same_v<Order, RowOrder>;
     GroupSmem<STAGES>& gs = *reinterpret_cast<GroupSmem<STAGES>*>(tiles + STAGES * STAGE_BYTES);
-    build_groups(gs.table, p.group_offsets, p.group_step, p.groups, p.group_T, 128, lane);
+    build_groups(gs.table, p.group_offsets, p.groups, p.group_T, 128, lane);
     __syncwarp();
     int i = 0;
     for (TileWalk<STAGES> w(tiles_c); w.tr < tiles_r; w.next(), ++i) {
@@ -833,11 +838,20 @@ __device__ __forceinline__ void load_group_tiles(const GroupMaps& maps, const Qu
         int src = 0, n = 0;  // lane h: segment h's first source row, its rows
         if (lane < SEGS) {
             const int r = (w.tr * SEGS + lane) * SEG_ROWS;
-            const int e = group_of(gs.table.padded, p.groups, r);
-            if (e >= 0) {
-                const int at = r - gs.table.padded[e];
-                src = gs.table.row[e] + at;
-                n = min(SEG_ROWS, max(0, gs.table.size(e) - at));
+            if constexpr (kRow) {
+                const int first = gs.table.row[0], end = gs.table.row[p.groups];
+                src = first + r;
+                n = min(SEG_ROWS, max(0, end - src));
+                const int t = first + w.tr * SEGS * SEG_ROWS;  // the tile's first row; lane 1: its last
+                gs.span[s][lane] =
+                    max(0, group_of(gs.table.row, p.groups, lane == 0 ? t : min(t + SEGS * SEG_ROWS, end) - 1));
+            } else {
+                const int e = group_of(gs.table.padded, p.groups, r);
+                if (e >= 0) {
+                    const int at = r - gs.table.padded[e];
+                    src = gs.table.row[e] + at;
+                    n = min(SEG_ROWS, max(0, gs.table.size(e) - at));
+                }
             }
             gs.rows[s][lane] = n;
         }
@@ -882,6 +896,20 @@ __device__ __forceinline__ void load_group_tiles(const GroupMaps& maps, const Qu
 template <int STAGES, int STAGE_BYTES>
 __device__ __forceinline__ int group_seg_rows(const uint8_t* tiles, int s, int h) {
     return reinterpret_cast<const GroupSmem<STAGES>*>(tiles + STAGES * STAGE_BYTES)->rows[s][h];
+}
+
+// Along the rows: the padded layout's row of row `at`, counted from the first
+// group's first and in stage s's tile.
+template <int STAGES, int STAGE_BYTES>
+__device__ __forceinline__ int group_padded_row(const uint8_t* tiles, int s, int at) {
+    const GroupSmem<STAGES>& gs = *reinterpret_cast<const GroupSmem<STAGES>*>(tiles + STAGES * STAGE_BYTES);
+    const int t = gs.table.row[0] + at;
+    int lo = gs.span[s][0], hi = gs.span[s][1] + 1;  // row[lo] <= t < row[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (gs.table.row[mid] <= t) lo = mid; else hi = mid;
+    }
+    return gs.table.padded[lo] + t - gs.table.row[lo];
 }
 
 // Four words of eight consecutive rows of a column (row 2i in the low half of
@@ -1074,20 +1102,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
     for (TileWalk<STAGES> w(tiles_c, issued); w.tr < tiles_r; w.next()) {
         const int s = w.stage;
         if (!mbar_wait(&ring.full[s], w.phase)) break;
-        const int64_t row = (int64_t)w.tr * kRowTileRows + tid;
+        int64_t row = (int64_t)w.tr * kRowTileRows + tid;
         const int64_t col0 = (int64_t)w.tc * kRowTileCols;
         const uint32_t sbase = smem_u32(tiles) + (uint32_t)(s * STAGE_BYTES) + (kHoist ? 0u : (uint32_t)tid * 128u);
         uint32_t codes[kRowTileCols / 8];
         uint32_t scodes[kRowTileCols / 16];
         uint32_t scw = 0;
-        // rows in groups: this thread's row may be no group's (its codes and
-        // scales are zero), or the whole warp's
+        // rows in groups: this thread's row may be no group's, or the whole warp's
         bool none = false, nothing = false;
         const float amax_before = amax_acc;
         if constexpr (GROUPED) {
             const int n = group_seg_rows<STAGES, STAGE_BYTES>(tiles, s, warp >> 2);
             none = (tid & 127) >= n;
             nothing = ((warp & 3) << 5) >= n;
+            if (!AMAX_ONLY && !none)
+                row = group_padded_row<STAGES, STAGE_BYTES>(tiles, s, w.tr * kRowTileRows + tid);
         }
         if (nothing) {
             // nothing to read
@@ -1132,20 +1161,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
             }
         }
         }
-        if constexpr (GROUPED) {
-            if (none) {
-                amax_acc = amax_before;
-                scw = 0;
-#pragma unroll
-                for (int i = 0; i < kRowTileCols / 8; ++i) codes[i] = 0;
-#pragma unroll
-                for (int i = 0; i < kRowTileCols / 16; ++i) scodes[i] = 0;
-            }
-        }
+        if constexpr (GROUPED)
+            if (none) amax_acc = amax_before;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ring.empty[s]);
         if constexpr (!AMAX_ONLY) {
-            if (row < p.rows) {
+            if (GROUPED ? !none : row < p.rows) {
                 uint8_t* dst = p.codes + row * (p.k / 2) + col0 / 2;
                 if (col0 + kRowTileCols <= p.k) {
                     store_codes32(dst, codes, ((p.k / 2) & 15) == 0, p.codes, codes_extent(p));
@@ -1155,13 +1176,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
                         if (col0 + 8 * w < p.k) *chk(reinterpret_cast<uint32_t*>(dst) + w, p.codes, codes_extent(p)) = codes[w];
                 }
             }
-            if (row < rows_pad) {
+            if (GROUPED ? !none : row < rows_pad) {
                 // this row's 64 / NB scale bytes: a whole 4-byte atom word (NVFP4) or
                 // half of one (MXFP4); past the last column tile the rest of the word
                 // is padding and is written as zero.
                 const int64_t kb0 = col0 / NB;
                 const int64_t off =
-                    kHoist ? (2 * (int64_t)w.tr) * atom_row_bytes + (kb0 / 4) * 512 + sc_row_off
+                    kHoist && !GROUPED ? (2 * (int64_t)w.tr) * atom_row_bytes + (kb0 / 4) * 512 + sc_row_off
                            : ((row / 128) * (p.kb4 / 4) + kb0 / 4) * 512 + (row % 32) * 16 + ((row / 32) % 4) * 4;
                 if constexpr (NB == 16) {
                     if constexpr (kPacked)

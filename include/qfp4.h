@@ -432,7 +432,8 @@ int qfp4_rmsnorm_bwd(const void* dy, int64_t lddy, const void* h, int64_t ldh, c
  *
  * qfp4_quantize_grouped: exactly what qfp4_quantize gives for the bf16 matrix
  *   x' of qfp4_group_rows(T, E) rows that holds x (T x C, row stride ld) in the
- *   padded layout. Requirements: those of qfp4_quantize for x', C a multiple
+ *   padded layout; along ROW the codes and scales of rows that are no group's
+ *   are left as they were (no product reads them into a result). Requirements: those of qfp4_quantize for x', C a multiple
  *   of 8; workspace as qfp4_quantize. x is read where it lies.
  * qfp4_gemm_grouped: D[offsets[e] + i][n] = gA gB sum_k A(p_e + i, k) B_e(n, k)
  *   for the rows i of each group: A = x' quantized along ROW, D T x N (row

@@ -80,11 +80,21 @@ def test_quantize_is_that_of_the_padded_rows(name, fmt, rnd, had, axis):
     Q.status()
     helpers.assert_guards_intact(*guards)
     want = O.quantize(padded(x, sizes, off, T), fmt, rnd, had, axis, ROT, 3, SRS, 5)
-    assert np.array_equal(helpers.to_numpy_u8(q.codes), want.codes)
     nb = Q.BLOCK[fmt]
-    flat = helpers.to_numpy_u8(q.scales)
-    assert np.array_equal(helpers.unswizzle_scales(flat, rows, k, nb), want.scales)
-    assert helpers.padding_is_zero(flat, rows, k, nb)
+    codes, flat = helpers.to_numpy_u8(q.codes), helpers.to_numpy_u8(q.scales)
+    own = np.ones(rows, dtype=bool)
+    if axis == Q.ROW:  # rows that are no group's are left as they were
+        own[:] = False
+        for p, m in zip(starts(sizes), sizes):
+            own[p:p + m] = True
+        kb4 = (k // nb + 3) // 4 * 4
+        every = flat[helpers.atom_offset(rows, k // nb, np.arange(rows)[:, None], np.arange(kb4)[None, :])]
+        assert np.all(codes[~own] == helpers.GUARD_PATTERN) and np.all(every[~own] == helpers.GUARD_PATTERN)
+        assert not every[own][:, k // nb:].any()
+    else:
+        assert helpers.padding_is_zero(flat, rows, k, nb)
+    assert np.array_equal(codes[own], want.codes[own])
+    assert np.array_equal(helpers.unswizzle_scales(flat, rows, k, nb)[own], want.scales[own])
     assert q.tensor_scale.item() == np.float32(want.g)
     assert (q.rows, q.k, q.desc.had) == (rows, k, had)
 
@@ -449,7 +459,7 @@ def test_offsets_past_32_bits():
     q = Q.quantize_grouped(x, off, Q.NVFP4, Q.SR, Q.HAD_DET16, Q.ROW, amax_in=amax)
     q0 = Q.quantize(torch.cat((torch.zeros((p, C), dtype=torch.bfloat16, device="cuda"), x[cut:])), Q.NVFP4, Q.SR,
                     Q.HAD_DET16, Q.ROW, amax_in=amax)
-    assert torch.equal(q.codes[p:p + T - cut], q0.codes[p:]) and not q.codes[:p].any()
+    assert torch.equal(q.codes[p:p + T - cut], q0.codes[p:]) and not q.codes[:cut].any()
     del q, q0
     q = Q.quantize_grouped(x, off, Q.MXFP4, Q.RTN, Q.HAD_DET32, Q.COL)
     first = (T - cut) // 128 * 128 - 128  # of the second group's rows: its last whole segment and the rest

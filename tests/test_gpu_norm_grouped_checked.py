@@ -50,7 +50,10 @@ def run_cases(Q, dev):
             keep(f"layer{E}{name}", Q.linear_grouped_fwd(X, W, off, rec, seed),
                  *Q.linear_grouped_bwd(dY, X, W, off, rec, seed))
         for axis in (Q.ROW, Q.COL):
-            q = Q.quantize_grouped(X, off, Q.MXFP4, Q.SR, Q.HAD_RAND32, axis, seed)
+            Tp = Q.group_rows(T, E)
+            q = Q.empty_qtensor(Q.MXFP4, *((Tp, K) if axis == Q.ROW else (K, Tp)), dev)
+            q.codes.zero_(), q.scales.zero_()
+            Q.quantize_grouped(X, off, Q.MXFP4, Q.SR, Q.HAD_RAND32, axis, seed, out=q)
             keep(f"q{E}{axis}", q.codes, q.scales)
         rec = Q.recipe("NVIDIA_NVFP4")
         rec.dgrad.rnd_a = rec.wgrad.rnd_a = Q.RTN
