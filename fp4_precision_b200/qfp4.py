@@ -721,22 +721,25 @@ class RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, res, w, eps: float):
         C = x.shape[-1]
-        r2 = None if res is None else res.reshape(-1, C)
-        x2 = x.reshape(-1, C)
-        y, h, rstd, _ = rmsnorm_fwd(x2, w, eps, res=r2, h=None if res is not None else torch.empty_like(x2))
+        # tensors of their own, not views: a program may change y in place (h is
+        # kept for the backward pass, which refuses a changed one)
+        y, h = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for _ in range(2))
+        _, _, rstd, _ = rmsnorm_fwd(x.reshape(-1, C), w, eps, res=None if res is None else res.reshape(-1, C),
+                                    y=y.view(-1, C), h=h.view(-1, C))
         ctx.save_for_backward(h, w, rstd)
         ctx.has_res = res is not None
         ctx.set_materialize_grads(False)  # an output that nothing uses has no gradient
-        return y.view(x.shape), h.view(x.shape)
+        return y, h
 
     @staticmethod
     def backward(ctx, dy, dh):
         h, w, rstd = ctx.saved_tensors
         if dy is None:  # h alone was used: it is x + res
             return dh, dh if ctx.has_res else None, None, None
-        dx, dw = rmsnorm_bwd(dy.reshape(h.shape).contiguous(), h, w, rstd,
-                             dh=None if dh is None else dh.reshape(h.shape).contiguous())
-        dx = dx.view(dy.shape)
+        C = h.shape[-1]
+        dx = torch.empty(h.shape, dtype=h.dtype, device=h.device)
+        _, dw = rmsnorm_bwd(dy.reshape(-1, C).contiguous(), h.view(-1, C), w, rstd,
+                            dh=None if dh is None else dh.reshape(-1, C).contiguous(), dx=dx.view(-1, C))
         return dx, dx if ctx.has_res else None, dw.to(w.dtype), None
 
 

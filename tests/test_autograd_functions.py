@@ -1,0 +1,70 @@
+"""What the autograd functions promise around their kernels: outputs that a
+program may change, inputs of any strides, first derivatives only. On the CPU
+the kernels' calls are replaced by their formulas, so that the functions
+themselves run here; on a GPU they are the real ones."""
+import pytest
+import torch
+
+from fp4_precision_b200 import qfp4 as Q
+
+EPS = 1e-5
+DEVICES = ["cpu", pytest.param("cuda", marks=pytest.mark.gpu)]
+
+
+def usable(m):
+    """What the RMSNorm calls ask of a matrix's strides (include/qfp4.h)."""
+    assert m.dim() == 2 and m.stride(1) == 1 and m.stride(0) >= m.shape[1] and m.stride(0) % 8 == 0
+    assert m.data_ptr() % 16 == 0
+    return m
+
+
+def norm_fwd(x, w, eps, res=None, y=None, h=None, **_):
+    y, h = (torch.empty_like(x) if t is None else t for t in (y, h))
+    usable(x), usable(y), usable(h), w.view(-1)
+    v = (x.float() + (0 if res is None else usable(res).float())).bfloat16()
+    rstd = (v.float().square().mean(1) + eps).rsqrt()
+    h.copy_(v)
+    y.copy_((v.float() * rstd[:, None] * w.float()).bfloat16())
+    return y, h, rstd, None
+
+
+def norm_bwd(dy, h, w, rstd, dh=None, dx=None, **_):
+    g, hr = usable(dy).float() * w.float(), usable(h).float() * rstd[:, None]
+    d = rstd[:, None] * (g - hr * (g * hr).mean(1, keepdim=True)) + (0 if dh is None else usable(dh).float())
+    dx = torch.empty_like(dy) if dx is None else dx
+    usable(dx).copy_(d.bfloat16())
+    return dx, (dy.float() * hr).sum(0)
+
+
+@pytest.fixture(autouse=True)
+def formulas(request, monkeypatch):
+    if request.node.callspec.params["dev"] == "cpu":
+        monkeypatch.setattr(Q, "rmsnorm_fwd", norm_fwd)
+        monkeypatch.setattr(Q, "rmsnorm_bwd", norm_bwd)
+
+
+def draw(dev, *shape, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(shape, generator=g).bfloat16().to(dev)
+
+
+def norm_inputs(dev, R=6, C=32):
+    return [draw(dev, R, C, seed=s).requires_grad_() for s in (1, 2)] + [draw(dev, C, seed=3).requires_grad_()]
+
+
+@pytest.mark.parametrize("dev", DEVICES)
+@pytest.mark.parametrize("with_res", [True, False])
+def test_norm_output_may_be_changed_in_place(dev, with_res):
+    """y scaled in place (a dropout, say): the gradients are those of the scaled y; h's change is refused backward."""
+    x, r, w = norm_inputs(dev)
+    r = r if with_res else None
+    leaves = [t for t in (x, r, w) if t is not None]
+    dy = draw(dev, *x.shape, seed=4)
+    want = torch.autograd.grad(Q.RmsNorm.apply(x, r, w, EPS)[0], leaves, 2 * dy)
+    y, h = Q.RmsNorm.apply(x, r, w, EPS)
+    got = torch.autograd.grad(y.mul_(2), leaves, dy)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    y, h = Q.RmsNorm.apply(x, r, w, EPS)
+    h.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward(dy)
