@@ -715,8 +715,28 @@ class Fp4Linear(torch.autograd.Function):
         return dX.to(X.dtype), dW.to(W.dtype), None, None
 
 
+class _FirstOrder(torch.autograd.Function):
+    """The tensors that compute() gives, as functions of deps whose own
+    gradients are refused."""
+
+    @staticmethod
+    def forward(ctx, compute, *deps):
+        return compute()
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("these kernels have first derivatives only: a gradient made with create_graph=True cannot "
+                           "be differentiated again")
+
+
+def _first_order(compute, *deps):
+    """compute(), gradients that depend on deps. With create_graph=True they would count as constants, and a second
+    backward pass drop their part without a word; here it raises."""
+    return _FirstOrder.apply(compute, *deps) if torch.is_grad_enabled() else compute()
+
+
 class RmsNorm(torch.autograd.Function):
-    """(y, h) = (h / rms(h) * w, x + res) in bf16; res may be None."""
+    """(y, h) = (h / rms(h) * w, x + res) in bf16; res may be None. First derivatives only."""
 
     @staticmethod
     def forward(ctx, x, res, w, eps: float):
@@ -736,16 +756,22 @@ class RmsNorm(torch.autograd.Function):
         h, w, rstd = ctx.saved_tensors
         if dy is None:  # h alone was used: it is x + res
             return dh, dh if ctx.has_res else None, None, None
-        C = h.shape[-1]
-        dx = torch.empty(h.shape, dtype=h.dtype, device=h.device)
-        _, dw = rmsnorm_bwd(dy.reshape(-1, C).contiguous(), h.view(-1, C), w, rstd,
-                            dh=None if dh is None else dh.reshape(-1, C).contiguous(), dx=dx.view(-1, C))
-        return dx, dx if ctx.has_res else None, dw.to(w.dtype), None
+
+        def gradients():
+            C = h.shape[-1]
+            dx = torch.empty(h.shape, dtype=h.dtype, device=h.device)
+            _, dw = rmsnorm_bwd(dy.reshape(-1, C).contiguous(), h.view(-1, C), w, rstd,
+                                dh=None if dh is None else dh.reshape(-1, C).contiguous(), dx=dx.view(-1, C))
+            return dx, dw.to(w.dtype)
+
+        dx, dw = _first_order(gradients, dy, dh, h, w)
+        return dx, dx if ctx.has_res else None, dw, None
 
 
 class Fp4GroupedLinear(torch.autograd.Function):
     """y[t] = x[t] W_e^T over the rows t of group e, W [E, N, K] (bf16 inputs,
-    recipe + seed per call). Rows that are no group's give zeros."""
+    recipe + seed per call). Rows that are no group's give zeros. First
+    derivatives only."""
 
     @staticmethod
     def forward(ctx, X, W, offsets, rec: Recipe, seed: Seed):
@@ -757,7 +783,11 @@ class Fp4GroupedLinear(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dY):
         X, W, offsets = ctx.saved_tensors
-        dX = torch.zeros(X.shape, dtype=_dtype(ctx.rec.dx_dtype), device=X.device)
-        dX, dW = linear_grouped_bwd(dY.contiguous().to(torch.bfloat16), X.contiguous(), W.contiguous(), offsets,
-                                    ctx.rec, ctx.seed, dX=dX)
-        return dX.to(X.dtype), dW.to(W.dtype), None, None, None
+
+        def gradients():
+            dX = torch.zeros(X.shape, dtype=_dtype(ctx.rec.dx_dtype), device=X.device)
+            _, dW = linear_grouped_bwd(dY.contiguous().to(torch.bfloat16), X.contiguous(), W.contiguous(), offsets,
+                                       ctx.rec, ctx.seed, dX=dX)
+            return dX.to(X.dtype), dW.to(W.dtype)
+
+        return *_first_order(gradients, dY, X, W), None, None, None

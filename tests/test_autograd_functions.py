@@ -36,11 +36,27 @@ def norm_bwd(dy, h, w, rstd, dh=None, dx=None, **_):
     return dx, (dy.float() * hr).sum(0)
 
 
+def grouped_fwd(X, W, offsets, rec, seed, Y=None, **_):
+    for e, (a, b) in enumerate(zip(offsets.tolist(), offsets.tolist()[1:])):
+        Y[a:b] = X[a:b] @ W[e].T
+    return Y
+
+
+def grouped_bwd(dY, X, W, offsets, rec, seed, dX=None, **_):
+    dW = torch.zeros(W.shape)
+    for e, (a, b) in enumerate(zip(offsets.tolist(), offsets.tolist()[1:])):
+        dX[a:b] = dY[a:b] @ W[e]
+        dW[e] = (dY[a:b].T @ X[a:b]).float()
+    return dX, dW
+
+
 @pytest.fixture(autouse=True)
 def formulas(request, monkeypatch):
     if request.node.callspec.params["dev"] == "cpu":
         monkeypatch.setattr(Q, "rmsnorm_fwd", norm_fwd)
         monkeypatch.setattr(Q, "rmsnorm_bwd", norm_bwd)
+        monkeypatch.setattr(Q, "linear_grouped_fwd", grouped_fwd)
+        monkeypatch.setattr(Q, "linear_grouped_bwd", grouped_bwd)
 
 
 def draw(dev, *shape, seed=0):
@@ -68,3 +84,46 @@ def test_norm_output_may_be_changed_in_place(dev, with_res):
     h.add_(1)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward(dy)
+
+
+def grouped_inputs(dev, T=5, E=2, N=128, K=128):
+    offsets = torch.tensor([0, 3, T], dtype=torch.int32, device=dev)
+    return draw(dev, T, K, seed=5).requires_grad_(), draw(dev, E, N, K, seed=6).requires_grad_(), offsets
+
+
+def norm_of_x(dev):
+    x, r, w = norm_inputs(dev)
+    return Q.RmsNorm.apply(x, r, w, EPS)[0], (x, r, w)
+
+
+def norm_and_stream(dev):
+    x, r, w = norm_inputs(dev)
+    y, h = Q.RmsNorm.apply(x, r, w, EPS)
+    return y.float() + h.float(), (x, r, w)
+
+
+def norm_alone(dev):
+    x, _, w = norm_inputs(dev)
+    return Q.RmsNorm.apply(x, None, w, EPS)[0], (x, w)
+
+
+def experts(dev):
+    X, W, offsets = grouped_inputs(dev)
+    return Q.Fp4GroupedLinear.apply(X, W, offsets, Q.recipe("AMD_MXFP4_H"), Q.make_seed()), (X, W)
+
+
+@pytest.mark.parametrize("dev", DEVICES)
+@pytest.mark.parametrize("f", [norm_of_x, norm_and_stream, norm_alone, experts])
+def test_second_derivatives_are_refused(dev, f):
+    """A penalty on the gradient, beside a path that has a second derivative: an error, where the function's part would
+    be missing from the sum. A gradient made with create_graph=True has the values of one made without."""
+    out, leaves = f(dev)
+    want = torch.autograd.grad(out.float().sum(), leaves)
+    out, leaves = f(dev)
+    grads = torch.autograd.grad(out.float().sum(), leaves, create_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(grads, want))
+    for g, t in zip(grads, leaves):
+        with pytest.raises(RuntimeError, match="first derivatives only"):
+            torch.autograd.grad(g.float().square().sum() + t.float().square().sum(), t, retain_graph=True)
+    if dev == "cuda":
+        Q.status()
