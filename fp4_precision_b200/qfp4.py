@@ -699,22 +699,6 @@ def selftest_rounding(op: int, x: torch.Tensor, w: torch.Tensor | None = None, s
     return codes
 
 
-class Fp4Linear(torch.autograd.Function):
-    """y = x W^T with FP4 Fprop/Dgrad/Wgrad (bf16 inputs, recipe + seed per call)."""
-
-    @staticmethod
-    def forward(ctx, X, W, rec: Recipe, seed: Seed):
-        ctx.save_for_backward(X, W)
-        ctx.rec, ctx.seed = rec, seed
-        return linear_fwd(X.contiguous(), W.contiguous(), rec, seed)
-
-    @staticmethod
-    def backward(ctx, dY):
-        X, W = ctx.saved_tensors
-        dX, dW = linear_bwd(dY.contiguous().to(torch.bfloat16), X.contiguous(), W.contiguous(), ctx.rec, ctx.seed)
-        return dX.to(X.dtype), dW.to(W.dtype), None, None
-
-
 class _FirstOrder(torch.autograd.Function):
     """The tensors that compute() gives, as functions of deps whose own
     gradients are refused."""
@@ -733,6 +717,27 @@ def _first_order(compute, *deps):
     """compute(), gradients that depend on deps. With create_graph=True they would count as constants, and a second
     backward pass drop their part without a word; here it raises."""
     return _FirstOrder.apply(compute, *deps) if torch.is_grad_enabled() else compute()
+
+
+class Fp4Linear(torch.autograd.Function):
+    """y = x W^T with FP4 Fprop/Dgrad/Wgrad (bf16 inputs, recipe + seed per
+    call). First derivatives only."""
+
+    @staticmethod
+    def forward(ctx, X, W, rec: Recipe, seed: Seed):
+        ctx.save_for_backward(X, W)
+        ctx.rec, ctx.seed = rec, seed
+        return linear_fwd(X.contiguous(), W.contiguous(), rec, seed)
+
+    @staticmethod
+    def backward(ctx, dY):
+        X, W = ctx.saved_tensors
+
+        def gradients():
+            dX, dW = linear_bwd(dY.contiguous().to(torch.bfloat16), X.contiguous(), W.contiguous(), ctx.rec, ctx.seed)
+            return dX.to(X.dtype), dW.to(W.dtype)
+
+        return *_first_order(gradients, dY, X, W), None, None
 
 
 class RmsNorm(torch.autograd.Function):

@@ -55,6 +55,8 @@ def formulas(request, monkeypatch):
     if request.node.callspec.params["dev"] == "cpu":
         monkeypatch.setattr(Q, "rmsnorm_fwd", norm_fwd)
         monkeypatch.setattr(Q, "rmsnorm_bwd", norm_bwd)
+        monkeypatch.setattr(Q, "linear_fwd", lambda X, W, *_: X @ W.T)
+        monkeypatch.setattr(Q, "linear_bwd", lambda dY, X, W, *_: (dY @ W, (dY.T @ X).float()))
         monkeypatch.setattr(Q, "linear_grouped_fwd", grouped_fwd)
         monkeypatch.setattr(Q, "linear_grouped_bwd", grouped_bwd)
 
@@ -112,8 +114,13 @@ def experts(dev):
     return Q.Fp4GroupedLinear.apply(X, W, offsets, Q.recipe("AMD_MXFP4_H"), Q.make_seed()), (X, W)
 
 
+def layer(dev):
+    X, W = (draw(dev, 128, 128, seed=s).requires_grad_() for s in (7, 8))
+    return Q.Fp4Linear.apply(X, W, Q.recipe("AMD_MXFP4_H"), Q.make_seed()), (X, W)
+
+
 @pytest.mark.parametrize("dev", DEVICES)
-@pytest.mark.parametrize("f", [norm_of_x, norm_and_stream, norm_alone, experts])
+@pytest.mark.parametrize("f", [norm_of_x, norm_and_stream, norm_alone, experts, layer])
 def test_second_derivatives_are_refused(dev, f):
     """A penalty on the gradient, beside a path that has a second derivative: an error, where the function's part would
     be missing from the sum. A gradient made with create_graph=True has the values of one made without."""
