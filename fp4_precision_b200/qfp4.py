@@ -740,6 +740,16 @@ class Fp4Linear(torch.autograd.Function):
         return *_first_order(gradients, dY, X, W), None, None
 
 
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """t as a matrix of its last dimension's rows; a copy where the kernels do
+    not take its strides or its address."""
+    m = t.reshape(-1, t.shape[-1])
+    if m.is_contiguous():
+        return m if m.data_ptr() % 16 == 0 else m.clone()
+    taken = m.stride(1) == 1 and m.stride(0) >= m.shape[1] and m.stride(0) % 8 == 0 and m.data_ptr() % 16 == 0
+    return m if taken else m.contiguous()
+
+
 class RmsNorm(torch.autograd.Function):
     """(y, h) = (h / rms(h) * w, x + res) in bf16; res may be None. First derivatives only."""
 
@@ -749,7 +759,7 @@ class RmsNorm(torch.autograd.Function):
         # tensors of their own, not views: a program may change y in place (h is
         # kept for the backward pass, which refuses a changed one)
         y, h = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for _ in range(2))
-        _, _, rstd, _ = rmsnorm_fwd(x.reshape(-1, C), w, eps, res=None if res is None else res.reshape(-1, C),
+        _, _, rstd, _ = rmsnorm_fwd(_rows(x), _rows(w)[0], eps, res=None if res is None else _rows(res),
                                     y=y.view(-1, C), h=h.view(-1, C))
         ctx.save_for_backward(h, w, rstd)
         ctx.has_res = res is not None
@@ -765,8 +775,8 @@ class RmsNorm(torch.autograd.Function):
         def gradients():
             C = h.shape[-1]
             dx = torch.empty(h.shape, dtype=h.dtype, device=h.device)
-            _, dw = rmsnorm_bwd(dy.reshape(-1, C).contiguous(), h.view(-1, C), w, rstd,
-                                dh=None if dh is None else dh.reshape(-1, C).contiguous(), dx=dx.view(-1, C))
+            _, dw = rmsnorm_bwd(_rows(dy), h.view(-1, C), _rows(w)[0], rstd, dh=None if dh is None else _rows(dh),
+                                dx=dx.view(-1, C))
             return dx, dw.to(w.dtype)
 
         dx, dw = _first_order(gradients, dy, dh, h, w)

@@ -20,7 +20,7 @@ def usable(m):
 
 def norm_fwd(x, w, eps, res=None, y=None, h=None, **_):
     y, h = (torch.empty_like(x) if t is None else t for t in (y, h))
-    usable(x), usable(y), usable(h), w.view(-1)
+    usable(x), usable(y), usable(h), usable(w.view(1, -1))
     v = (x.float() + (0 if res is None else usable(res).float())).bfloat16()
     rstd = (v.float().square().mean(1) + eps).rsqrt()
     h.copy_(v)
@@ -132,5 +132,41 @@ def test_second_derivatives_are_refused(dev, f):
     for g, t in zip(grads, leaves):
         with pytest.raises(RuntimeError, match="first derivatives only"):
             torch.autograd.grad(g.float().square().sum() + t.float().square().sum(), t, retain_graph=True)
+    if dev == "cuda":
+        Q.status()
+
+
+def apart(t, at):
+    """t's values where each lies `at` elements behind the one before it."""
+    held = torch.zeros(t.numel() * at, dtype=t.dtype, device=t.device)
+    return held.as_strided(t.shape, (t.shape[1] * at, at)).copy_(t)
+
+
+ORDERS = {
+    "transposed": lambda t: t.t().contiguous().t(),
+    "every other element": lambda t: apart(t, 2),
+    "rows 20 bytes further apart": lambda t: torch.cat((t, t[:, :10]), 1)[:, :t.shape[1]],
+    "an odd address": lambda t: torch.cat((t[:1, :1].flatten(), t.flatten()))[1:].view(t.shape),
+    "one row for all": lambda t: t[:1].expand(t.shape),
+    "a slice": lambda t: torch.cat((t, t), 1)[:, t.shape[1]:],
+}
+
+
+@pytest.mark.parametrize("dev", DEVICES)
+@pytest.mark.parametrize("order", ORDERS)
+def test_norm_takes_any_strides(dev, order):
+    """x, the residual, the weight and both gradients in other orders: what contiguous ones give."""
+    lay = ORDERS[order]
+    x, r, dy, dh = (lay(draw(dev, 6, 32, seed=s)) for s in (11, 12, 13, 14))
+    w = draw(dev, 32, 3, seed=15)[:, 1]
+
+    def run(*ts):
+        a, b, c, *gs = (t.detach() for t in ts)
+        leaves = [t.requires_grad_() for t in (a, b, c)]
+        out = Q.RmsNorm.apply(*leaves, EPS)
+        return (*out, *torch.autograd.grad(out, leaves, gs))
+
+    got, want = run(x, r, w, dy, dh), run(*(t.contiguous().clone() for t in (x, r, w, dy, dh)))
+    assert all(a.is_contiguous() and torch.equal(a, b) for a, b in zip(got, want))
     if dev == "cuda":
         Q.status()
