@@ -466,9 +466,11 @@ def _ref(seed: Seed | None):
 
 
 def _workspace(given, nbytes: int, like: torch.Tensor):
-    """Address and size of a workspace, and the tensor that holds it."""
+    """Address and size of a workspace on like's GPU, and the tensor that holds it."""
     if given is None:
         given = like.new_empty((nbytes,), dtype=torch.uint8)
+    else:
+        assert given.is_contiguous() and given.get_device() == like.get_device(), "a workspace on the tensors' GPU"
     return given.data_ptr(), given.numel() * given.element_size(), given
 
 
