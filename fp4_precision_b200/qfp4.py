@@ -461,6 +461,17 @@ def _new_qtensor(like: torch.Tensor, fmt: int, rows: int, k: int) -> QTensor:
     return QTensor(codes, scales, ts, TensorDesc(codes.data_ptr(), scales.data_ptr(), ts.data_ptr()))
 
 
+def _operand(q: QTensor, fmt: int, rows: int, k: int, i: int) -> QTensor:
+    """Check that q's buffers, the ones its descriptor names, hold a rows x k operand on GPU i."""
+    parts = (q.codes, codes_bytes(rows, k)), (q.scales, scales_bytes(fmt, rows, k)), (q.tensor_scale, 4)
+    for t, nbytes in parts:
+        assert t.is_contiguous() and t.get_device() == i, "an operand's buffers on the tensors' GPU"
+        assert t.numel() * t.element_size() >= nbytes, f"a buffer of {nbytes} bytes for a {rows} x {k} operand"
+    named = (q.desc.codes, q.desc.scales, q.desc.tensor_scale)
+    assert all((a or 0) == t.data_ptr() for a, (t, _) in zip(named, parts)), "a descriptor of the operand's buffers"
+    return q
+
+
 def _ref(seed: Seed | None):
     return None if seed is None else ctypes.byref(seed)
 
@@ -534,7 +545,7 @@ def rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, eps: float, res: torch.Te
         y = torch.empty_like(x)
     h, hp, ldh, rp, ldr = _residual(x, res, h, shape, i)
     rstd = x.new_empty((R,), dtype=torch.float32) if rstd is None else rstd
-    out = _new_qtensor(x, MXFP4, R, C) if out is None else out
+    out = _new_qtensor(x, MXFP4, R, C) if out is None else _operand(out, MXFP4, R, C, i)
     _go(lib().qfp4_rmsnorm_quantize, "qfp4_rmsnorm_quantize", i, x.data_ptr(), ldx, rp, ldr,
         _vector(w, C, torch.bfloat16, i), R, C, eps, hp, ldh, None if y is None else y.data_ptr(),
         0 if y is None else _matrix(y, shape, i), _vector(rstd, R, torch.float32, i), fmt, had, _ref(seed),
@@ -587,9 +598,9 @@ def quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, fmt: int, rounding:
     ldx = _matrix(x, shape, i)
     T, C = shape
     E = _groups(offsets, i)
-    if out is None:
-        Tp = max(group_rows(T, E), 0)
-        out = _new_qtensor(x, fmt, *((Tp, C) if axis == ROW else (C, Tp)))
+    Tp = max(group_rows(T, E), 0)
+    rows, k = (Tp, C) if axis == ROW else (C, Tp)
+    out = _new_qtensor(x, fmt, rows, k) if out is None else _operand(out, fmt, rows, k, i)
     wsp, wsb = None, 0
     if amax_in is None and fmt == NVFP4:
         wsp, wsb, workspace = _workspace(workspace, 4 * _WS_FLOATS, x)

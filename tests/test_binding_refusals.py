@@ -6,7 +6,7 @@ import torch
 
 from fp4_precision_b200 import qfp4 as Q
 
-T, E, N, K, R, C = 40, 3, 128, 128, 4, 64
+T, E, N, K, R, C = 100, 3, 128, 128, 4, 64  # 384 rows of the padded layout
 
 
 class OnGpu0(torch.Tensor):
@@ -67,3 +67,34 @@ def test_workspaces(calls, name):
     WITH_WORKSPACE[name](workspace=gpu(BYTES, dtype=torch.uint8))
     WITH_WORKSPACE[name](workspace=None)
     assert calls == 2 * ["qfp4_" + name]
+
+
+def operand(fmt, rows, k, **other):
+    """Buffers for a rows x k operand, or with `other` ones in their place."""
+    parts = dict(codes=gpu(rows, k // 2, dtype=torch.uint8), scales=gpu(Q.scales_bytes(fmt, rows, k), dtype=torch.uint8),
+                 tensor_scale=gpu(1, dtype=torch.float32))
+    named = Q.TensorDesc(*(t.data_ptr() for t in {**parts, **other}.values()))
+    return Q.QTensor(**{**parts, **other}, desc=named)
+
+
+@pytest.mark.parametrize("name,fmt,rows,k,less,call", [
+    ("rmsnorm_quantize", Q.MXFP4, R, C, R - 1, lambda q: Q.rmsnorm_quantize(X0, gpu(C), 1e-5, out=q)),
+    ("quantize_grouped", Q.NVFP4, 384, K, T, lambda q: Q.quantize_grouped(X, OFF, Q.NVFP4, Q.RTN, 0, Q.ROW, out=q)),
+    ("quantize_grouped", Q.MXFP4, K, 384, K - 1, lambda q: Q.quantize_grouped(X, OFF, Q.MXFP4, Q.RTN, 0, Q.COL, out=q)),
+])
+def test_operand_buffers(calls, name, fmt, rows, k, less, call):
+    """Buffers that are too small (x's own rows, say, in place of the padded layout's) or not on the tensors' GPU."""
+    good = operand(fmt, rows, k)
+    bad = [operand(fmt, rows, k, codes=gpu(less, k // 2, dtype=torch.uint8)),
+           operand(fmt, rows, k, scales=gpu(good.scales.numel() - 1, dtype=torch.uint8)),
+           operand(fmt, rows, k, tensor_scale=gpu(0, dtype=torch.float32)),
+           operand(fmt, rows, k, codes=torch.zeros((rows, k // 2), dtype=torch.uint8)),
+           operand(fmt, rows, k, scales=gpu(good.scales.numel(), dtype=torch.uint8, cls=OnGpu1)),
+           operand(fmt, rows, k, codes=gpu(rows, k, dtype=torch.uint8)[:, ::2]),
+           Q.QTensor(good.codes.clone(), good.scales, good.tensor_scale, good.desc)]
+    for q in bad:
+        with pytest.raises(AssertionError):
+            call(q)
+    assert not calls
+    assert call(good) is good or call(good)[3] is good
+    assert calls[0] == "qfp4_" + name
