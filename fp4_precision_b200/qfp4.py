@@ -415,6 +415,8 @@ def _on_stream(f):
         stream = kwargs.pop("stream")
         if stream is None:
             return f(*args, **kwargs)
+        t = next(a for a in (*args, *kwargs.values()) if isinstance(a, (torch.Tensor, QTensor)))
+        assert stream.device.index == _gpu(t.codes if isinstance(t, QTensor) else t), "a stream of the tensors' GPU"
         with torch.cuda.stream(stream):
             return f(*args, **kwargs)
     return call

@@ -1,6 +1,8 @@
 """What the RMSNorm and grouped calls of the binding refuse before they reach the
 library: buffers and streams that are not the tensors' GPU's. Tensors here only
 say that they are on a GPU, so this runs without one."""
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -98,3 +100,29 @@ def test_operand_buffers(calls, name, fmt, rows, k, less, call):
     assert not calls
     assert call(good) is good or call(good)[3] is good
     assert calls[0] == "qfp4_" + name
+
+
+def quantized(rows, k):
+    q = operand(Q.NVFP4, rows, k)
+    q.desc.rows, q.desc.k = rows, k
+    return q
+
+
+STREAMED = WITH_WORKSPACE | {
+    "rmsnorm_quantize": lambda **k: Q.rmsnorm_quantize(w=gpu(C), x=X0, eps=1e-5, **k),
+    "gemm_grouped": lambda **k: Q.gemm_grouped(quantized(384, K), quantized(E * N, K), OFF, T, **k),
+    "gemm_grouped_wgrad": lambda **k: Q.gemm_grouped_wgrad(quantized(N, 384), quantized(K, 384), OFF, T, **k),
+}
+
+
+@pytest.mark.parametrize("name", STREAMED)
+def test_streams(calls, name):
+    """A stream of another GPU than the tensors' would not be the one that the call runs on."""
+    def stream(i):
+        return SimpleNamespace(device=torch.device("cuda", i))
+    with pytest.raises(AssertionError, match="stream"):
+        STREAMED[name](stream=stream(1))
+    assert not calls
+    STREAMED[name](stream=stream(0))
+    STREAMED[name](stream=None)
+    assert calls == 2 * ["qfp4_" + name]
