@@ -149,10 +149,16 @@ def _check(status: int, what: str):
         raise QFP4Error(status, what)
 
 
+# The current device and its stream without the objects around them, at every
+# call; torch's public calls where a version does not have these.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         torch.cuda.init()
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+        return ctypes.c_void_p(_current_stream(_current_device()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -423,8 +429,8 @@ def _on_stream(f):
 
 
 def _go(fn, what: str, i: int, *args):
-    h = torch._C._cuda_getCurrentRawStream(i)
-    if i == torch._C._cuda_getDevice():
+    h = _current_stream(i)
+    if i == _current_device():
         status = fn(*args, h)
     else:
         with torch.cuda.device(i):
