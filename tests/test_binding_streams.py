@@ -1,6 +1,7 @@
 """The current stream of the binding's calls, also where torch lacks the private
 names that it takes it from."""
 import importlib.util
+import sys
 from types import SimpleNamespace
 
 import pytest
@@ -13,11 +14,13 @@ PRIVATE = ("_cuda_getCurrentRawStream", "_cuda_getDevice")
 
 def binding_without(monkeypatch, names):
     """The binding as imported where torch._C lacks `names`."""
-    for n in names:
-        monkeypatch.delattr(torch._C, n, raising=False)
     spec = importlib.util.spec_from_file_location("fp4_precision_b200.qfp4_plain", Q.__file__)
-    monkeypatch.setitem(__import__("sys").modules, spec.name, m := importlib.util.module_from_spec(spec))
-    spec.loader.exec_module(m)
+    m = importlib.util.module_from_spec(spec)
+    with monkeypatch.context() as without:  # (torch itself uses them)
+        without.setitem(sys.modules, spec.name, m)
+        for n in names:
+            without.delattr(torch._C, n, raising=False)
+        spec.loader.exec_module(m)
     return m
 
 
