@@ -391,7 +391,9 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_bwd_ring_kernel(const NormBwd
     ring.init(p.stages);
     pdl_wait();
     pdl_launch_dependents();
+    int issued = 0;
     auto fetch = [&](int64_t row, int s) {  // one thread
+        ++issued;
         uint8_t* d = dyn_smem + s * parts * row_bytes;
         mbar_arrive_expect_tx(&ring.full[s], parts * row_bytes);
         bulk_load(d, p.dy + row * p.lddy, row_bytes, &ring.full[s]);
@@ -431,6 +433,7 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_bwd_ring_kernel(const NormBwd
         }
     }
     th.write_dw(p, blockIdx.x, gridDim.x);
+    if (threadIdx.x == 0) drain_loads(ring.full, nullptr, p.stages, issued);  // no copy lands after this CTA exits
 }
 
 // dw[c] (+)= the sum of column c of the n partial rows, in a fixed order: 32
