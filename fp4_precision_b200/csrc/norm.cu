@@ -258,12 +258,13 @@ __global__ void __launch_bounds__(WARP_ROW ? 128 : 512) rmsnorm_fwd_kernel(const
 // fill with one row each of up to three tensors.
 struct NormRing {
     uint64_t full[kNormMaxStages];
-    int dead;  // a wait ran out
+    int dead[2];  // a wait ran out; for even and odd rows in turn, so that a
+                  // thread a row ahead does not change what this row's threads read
     __device__ __forceinline__ void init(int stages) {
         if (threadIdx.x == 0) {
             for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
             fence_mbarrier_init();
-            dead = 0;
+            dead[0] = dead[1] = 0;
         }
         __syncthreads();
     }
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_bwd_ring_kernel(const NormBwd
     for (int64_t row = blockIdx.x; row < p.R; row += gridDim.x, parity ^= 1) {
         const float rstd = rstd1;
         if (row + gridDim.x < p.R) rstd1 = p.rstd[row + gridDim.x];
-        if (!mbar_wait(&ring.full[s], phase)) ring.dead = 1;  // seen by all behind the barrier
+        if (!mbar_wait(&ring.full[s], phase)) ring.dead[parity] = 1;  // seen by all behind the barrier
         const uint16_t* d = reinterpret_cast<const uint16_t*>(dyn_smem + s * parts * row_bytes);
         uint32_t dy[4 * NV], h[4 * NV], dh[4 * NV];
         th.load(d, dy);
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_bwd_ring_kernel(const NormBwd
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) red[parity][warp] = sum;
         __syncthreads();  // the sums are written, and the stage is read
-        if (ring.dead) break;
+        if (ring.dead[parity]) break;
         if (threadIdx.x == 0 && row + (int64_t)p.stages * gridDim.x < p.R) fetch(row + (int64_t)p.stages * gridDim.x, s);
         sum = red[parity][0];
         for (int w = 1; w < warps; ++w) sum += red[parity][w];

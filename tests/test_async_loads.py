@@ -53,3 +53,12 @@ def test_copies_are_waited_for(file, name):
     body = next(b for f, n, b in KERNELS if (f, n) == (file, name))
     if STARTS.search(body):
         assert "drain_loads(" in body
+
+
+def test_threads_of_a_cta_leave_at_the_same_row():
+    """The ring's flag is set before the barrier of a row and read behind it. A thread that is a row ahead may set it
+    while others still read, so rows take turns at two flags."""
+    body = next(b for _, n, b in KERNELS if n == "rmsnorm_bwd_ring_kernel")
+    uses = re.findall(r"ring\.dead(\[parity\])?", body)
+    assert len(uses) == 2 and all(uses)
+    assert body.index("ring.dead[parity] = 1") < body.index("__syncthreads()") < body.index("if (ring.dead[parity]) break")
