@@ -94,11 +94,13 @@ __device__ __forceinline__ void group_epilogue(const GroupedParams& p, const CUt
                                                Release release) {
     // 32 words (128 bytes) of each lane's row, from column x: a whole box of 32
     // rows through shared memory (128-byte swizzle) by TMA, which clips the
-    // columns past N
+    // columns past N. The warp leaves it together: the next loads from tensor
+    // memory are the whole warp's.
     const uint32_t rbase = obox + (uint32_t)lane * 128u;
     auto box = [&](const uint32_t* v, int x) {
         if (nv < 32) {
             if (lane < nv) store_row_words(p, v, row + lane, x);
+            __syncwarp();
             return;
         }
         if (lane == 0) bulk_wait_group_read0();  // the box's last store has read it
@@ -115,6 +117,7 @@ __device__ __forceinline__ void group_epilogue(const GroupedParams& p, const CUt
                 tma_store_2d(tmD, obox, x, row);
             bulk_commit_group();
         }
+        __syncwarp();
     };
     if (!p.out_f32) {
         uint32_t w[64];
@@ -525,17 +528,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(acc_empty);
                 }
-                if (!mine) continue;
-                if (!p.out_f32) {
+                if (mine) {
+                    if (!p.out_f32) {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) acc[c] = pack_bf16(acc[2 * c], acc[2 * c + 1], scale);
-                    store_row_words(p, acc, row, n0 + 64 * h);
-                } else {
+                        for (int c = 0; c < 32; ++c) acc[c] = pack_bf16(acc[2 * c], acc[2 * c + 1], scale);
+                        store_row_words(p, acc, row, n0 + 64 * h);
+                    } else {
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) acc[c] = __float_as_uint(__fmul_rn(__uint_as_float(acc[c]), scale));
-                    store_row_words(p, acc, row, n0 + 64 * h);
-                    store_row_words(p, acc + 32, row, n0 + 64 * h + 32);
+                        for (int c = 0; c < 64; ++c) acc[c] = __float_as_uint(__fmul_rn(__uint_as_float(acc[c]), scale));
+                        store_row_words(p, acc, row, n0 + 64 * h);
+                        store_row_words(p, acc + 32, row, n0 + 64 * h + 32);
+                    }
                 }
+                __syncwarp();  // the next loads from tensor memory are the whole warp's
             }
         }
     }
