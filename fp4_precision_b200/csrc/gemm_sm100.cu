@@ -315,7 +315,9 @@ __device__ __forceinline__ void store_f32(const GemmParams& p, uint32_t* acc, in
 // Epilogue of one tile for one warp: 128 accumulator columns of its lane
 // quarter. The accumulator goes back to the MMA warp (release()) as soon as
 // the values are in registers: all 128 columns for bf16 output (packed, 64
-// registers), the last 96 for fp32 after the first 32 are stored.
+// registers), the last 96 for fp32 after the first 32 are stored. Lanes past the
+// matrix store nothing; the warp meets again before its next loads from tensor
+// memory, which are the whole warp's.
 template <typename Release>
 __device__ __forceinline__ void epilogue_tile(const GemmParams& p, uint32_t taddr, int row, int n0, float scale,
                                               Release release) {
@@ -334,6 +336,7 @@ __device__ __forceinline__ void epilogue_tile(const GemmParams& p, uint32_t tadd
 #pragma unroll
             for (int c = 0; c < 8; ++c) w[c] = pack_bf16(acc[2 * c], acc[2 * c + 1], scale);
             if (n0 + 16 * h < p.N) store_bf16_edge<16>(p, w, row, n0 + 16 * h);
+            __syncwarp();
         }
     } else if (!p.out_f32) {
         uint32_t w[64];
@@ -350,12 +353,14 @@ __device__ __forceinline__ void epilogue_tile(const GemmParams& p, uint32_t tadd
         __syncwarp();
         release();
         store_bf16<128>(p, w, row, n0);
+        __syncwarp();
     } else {
         uint32_t acc[80];
         tmem_ld_32x32b_x16(taddr, acc);
         tmem_ld_32x32b_x32(taddr + 16, acc + 16);
         tc_wait_ld();
         store_f32<48>(p, acc, row, n0, scale);
+        __syncwarp();
         tmem_ld_32x32b_x16(taddr + 48, acc);
         tmem_ld_32x32b_x32(taddr + 64, acc + 16);
         tmem_ld_32x32b_x32(taddr + 96, acc + 48);
@@ -364,6 +369,7 @@ __device__ __forceinline__ void epilogue_tile(const GemmParams& p, uint32_t tadd
         __syncwarp();
         release();
         store_f32<80>(p, acc, row, n0 + 48, scale);
+        __syncwarp();
     }
 }
 
@@ -478,6 +484,7 @@ __device__ __forceinline__ void epilogue_tile_tma(const GemmParams& p, const CUt
         if (n0 < p.N) quantize_out_row128<NHQ>(p, w, row0 + lane, n0);
     }
     if constexpr (AMX >= 0) amax_acc = row128_rot_amax<AMX>(w, p.amax_signs, amax_acc);
+    __syncwarp();
 }
 
 // fp32 output: the same with boxes of 32 rows x 32 columns (128-byte rows),
@@ -506,6 +513,7 @@ __device__ __forceinline__ void box_f32(const GemmParams& p, const CUtensorMap* 
             tma_store_2d(tmD, obox, x, row0);
         bulk_commit_group();
     }
+    __syncwarp();
 }
 template <typename Release>
 __device__ __forceinline__ void epilogue_tile_tma_f32(const GemmParams& p, const CUtensorMap* tmD, uint32_t taddr,
