@@ -1321,6 +1321,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t stage_base = smem_u32(tiles) + (uint32_t)(s * STAGE_BYTES);
         int valid = G;  // rows in groups: of this thread's G rows, those that are the group's
         if constexpr (GROUPED) valid = group_seg_rows<STAGES, STAGE_BYTES>(tiles, s, 0) - G * q;
+        const bool cut = GROUPED && __any_sync(0xffffffffu, valid < G);  // (the loads below are the whole warp's)
         if constexpr (kSharedQuads) {
             if (shared_quads && quad_half == 0) {
                 int qtr = w.tr, qtc = w.tc;
@@ -1349,7 +1350,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                              : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
                              : "r"(addr));
                 if constexpr (GROUPED) {
-                    if (valid < G) {
+                    if (cut) {
                         const uint4 m = mask_rows8(make_uint4(a0, a1, a2, a3), valid - 8 * u);
                         a0 = m.x; a1 = m.y; a2 = m.z; a3 = m.w;
                     }
@@ -1710,6 +1711,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
         const uint32_t stage_base = smem_u32(tiles) + (uint32_t)(s * STAGE_BYTES) + lm_base;
         int valid = 64;  // rows in groups: of this thread's band, those that are the group's
         if constexpr (GROUPED) valid = group_seg_rows<STAGES, STAGE_BYTES>(tiles, s, q >> 1) - 64 * (q & 1);
+        const bool cut = GROUPED && __any_sync(0xffffffffu, valid < 64);  // (the loads below are the whole warp's)
         uint32_t codes[8];
         uint32_t scodes[64 / NB];
         uint32_t scw = 0;
@@ -1721,7 +1723,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
                              : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                              : "r"(stage_base + (uint32_t)n * kLmStep));
                 if constexpr (GROUPED)
-                    if (valid < 64) v = mask_rows8(v, valid - 8 * n);
+                    if (cut) v = mask_rows8(v, valid - 8 * n);
                 return v;
             };
             scw = nv64_quantize<RND, NH>(load, sf, s_enc, tab2, col_stream(p), (uint64_t)c * (uint64_t)p.k + (uint64_t)rb,
@@ -1738,7 +1740,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
                              : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
                              : "r"(addr));
                 if constexpr (GROUPED) {
-                    if (valid < 64) {
+                    if (cut) {
                         const uint4 m = mask_rows8(make_uint4(a0, a1, a2, a3), valid - 8 * (g * (G / 8) + u));
                         a0 = m.x; a1 = m.y; a2 = m.z; a3 = m.w;
                     }
@@ -1872,13 +1874,14 @@ __global__ void __launch_bounds__(kThreads, 2)
             valid = group_seg_rows<STAGES, STAGE_BYTES>(tiles, s, (lane & 3) >> 1) - 64 * (lane & 1);
             none = BandOrder::row(tid & 127) >= group_seg_rows<STAGES, STAGE_BYTES>(tiles, s, warp >> 2);
         }
+        const bool cut = GROUPED && __any_sync(0xffffffffu, valid < 64);  // (the loads below are the whole warp's)
         auto load_col = [&](int n) {
             uint4 v;
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                          : "r"(stage + lm_base + (uint32_t)n * kLmStep));
             if constexpr (GROUPED)
-                if (valid < 64) v = mask_rows8(v, valid - 8 * n);
+                if (cut) v = mask_rows8(v, valid - 8 * n);
             return v;
         };
         m_col = rot_amax64<NH>(load_col, sf_col, m_col);
