@@ -1230,7 +1230,8 @@ int set_zero(float* v, int64_t n, cudaStream_t s) {
 // ---- groups of rows -------------------------------------------------------------
 int check_groups(const int32_t* offsets, int32_t E, int64_t T) {
     if (E < 1 || E > QFP4_MAX_GROUPS || T < 0 || T > 0x7fffffffLL) return QFP4_ERR_INVALID_ARG;
-    if (group_rows(T, E) > 0x7fffffffLL || offsets == nullptr) return QFP4_ERR_INVALID_ARG;
+    // the kernels count rows up to the end of a tile past the last one in 32 bits
+    if (group_rows(T, E) > QFP4_MAX_GROUP_ROWS || offsets == nullptr) return QFP4_ERR_INVALID_ARG;
     return reinterpret_cast<uintptr_t>(offsets) % 4 == 0 ? QFP4_OK : QFP4_ERR_MISALIGNED;
 }
 

@@ -839,12 +839,14 @@ __device__ __forceinline__ void load_group_tiles(const GroupMaps& maps, const Qu
         if (lane < SEGS) {
             const int r = (w.tr * SEGS + lane) * SEG_ROWS;
             if constexpr (kRow) {
-                const int first = gs.table.row[0], end = gs.table.row[p.groups];
-                src = first + r;
-                n = min(SEG_ROWS, max(0, end - src));
-                const int t = first + w.tr * SEGS * SEG_ROWS;  // the tile's first row; lane 1: its last
-                gs.span[s][lane] =
-                    max(0, group_of(gs.table.row, p.groups, lane == 0 ? t : min(t + SEGS * SEG_ROWS, end) - 1));
+                // counted from the first group's first row: past it by T or more,
+                // sums with it would leave 32 bits
+                const int first = gs.table.row[0], rows = gs.table.row[p.groups] - first;
+                n = min(SEG_ROWS, max(0, rows - r));
+                src = n > 0 ? first + r : 0;
+                const int t = w.tr * SEGS * SEG_ROWS;  // the tile's first row; lane 1: its last
+                const int at = max(0, min(lane == 0 ? t : t + SEGS * SEG_ROWS - 1, rows - 1));
+                gs.span[s][lane] = max(0, group_of(gs.table.row, p.groups, first + at));
             } else {
                 const int e = group_of(gs.table.padded, p.groups, r);
                 if (e >= 0) {

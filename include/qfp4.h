@@ -423,7 +423,8 @@ int qfp4_rmsnorm_bwd(const void* dy, int64_t lddy, const void* h, int64_t ldh, c
  * offsets[E] on belong to no group and are neither read into a result nor
  * written. Sizes are read on the device, so calls can be captured and replayed
  * with other offsets. Offsets that break the rule count as all groups empty
- * and are reported by qfp4_status (QFP4_ERR_OFFSETS). 1 <= E <= QFP4_MAX_GROUPS.
+ * and are reported by qfp4_status (QFP4_ERR_OFFSETS). 1 <= E <= QFP4_MAX_GROUPS,
+ * qfp4_group_rows(T, E) <= QFP4_MAX_GROUP_ROWS.
  *
  * Padded layout: group e starts at row p_e = sum_{i<e} 128 ceil(m_i / 128) (m_i
  * rows in group i), in qfp4_group_rows(T, E) rows in all; every row that is no
@@ -462,6 +463,7 @@ int qfp4_rmsnorm_bwd(const void* dy, int64_t lddy, const void* h, int64_t ldh, c
  * (page "New AMD paper overturns conventional wisdom: FP4 training...",
  * section "Poiskovaya eksperimental'naya rabota"). */
 #define QFP4_MAX_GROUPS 256
+#define QFP4_MAX_GROUP_ROWS 0x7ffffc00LL /* 2^31 - 1024 */
 int64_t qfp4_group_rows(int64_t T, int32_t E); /* -1 for a bad E or T */
 int qfp4_quantize_grouped(const void* x, int64_t T, int64_t C, int64_t ld, const int32_t* offsets, int32_t E,
                           int32_t fmt, int32_t rounding, int32_t had, int32_t axis, const qfp4_seed* seed,
