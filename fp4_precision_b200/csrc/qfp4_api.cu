@@ -1303,7 +1303,7 @@ int gemm_grouped_impl(const qfp4_tensor* A, const qfp4_tensor* B, const int32_t*
     if ((rc = check_device(&sms))) return rc;
     GroupedParams p{};
     p.offsets = offsets;
-    p.E = E; p.T = (int)T; p.Tp = (int)A->rows;
+    p.E = E; p.T = (int)T;
     p.D = D;
     p.ldd = ldd;
     p.out_f32 = out_dtype == QFP4_OUT_F32;
@@ -1337,7 +1337,7 @@ int gemm_grouped_wgrad_impl(const qfp4_tensor* A, const qfp4_tensor* B, const in
     }
     GroupedParams p{};
     p.offsets = offsets;
-    p.E = E; p.T = (int)T; p.Tp = (int)Tp;
+    p.E = E; p.T = (int)T;
     p.D = D;
     p.ldd = N;
     p.out_f32 = out_dtype == QFP4_OUT_F32;

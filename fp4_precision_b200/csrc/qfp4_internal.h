@@ -189,10 +189,10 @@ cudaError_t launch_rmsnorm_bwd(NormBwdParams p, float* dw, int accumulate, int s
 
 // grouped_sm100.cu: rows in groups (the experts of a mixture). offsets: device
 // int32 [E + 1], group e's rows are [offsets[e], offsets[e + 1]) of T; in the
-// padded layout it starts at row sum_{i<e} 128 ceil(m_i / 128) of Tp.
+// padded layout it starts at row sum_{i<e} 128 ceil(m_i / 128).
 struct GroupedParams {
     const int* offsets;
-    int E, T, Tp;
+    int E, T;
     const float* ga;
     const float* gb;
     void* D;
