@@ -392,9 +392,7 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_bwd_ring_kernel(const NormBwd
     ring.init(p.stages);
     pdl_wait();
     pdl_launch_dependents();
-    int issued = 0;
     auto fetch = [&](int64_t row, int s) {  // one thread
-        ++issued;
         uint8_t* d = dyn_smem + s * parts * row_bytes;
         mbar_arrive_expect_tx(&ring.full[s], parts * row_bytes);
         bulk_load(d, p.dy + row * p.lddy, row_bytes, &ring.full[s]);
@@ -409,7 +407,8 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_bwd_ring_kernel(const NormBwd
     float rstd1 = blockIdx.x < p.R ? p.rstd[blockIdx.x] : 0.0f;
     int s = 0, parity = 0;
     uint32_t phase = 0;
-    for (int64_t row = blockIdx.x; row < p.R; row += gridDim.x, parity ^= 1) {
+    int64_t row = blockIdx.x;
+    for (; row < p.R; row += gridDim.x, parity ^= 1) {
         const float rstd = rstd1;
         if (row + gridDim.x < p.R) rstd1 = p.rstd[row + gridDim.x];
         if (!mbar_wait(&ring.full[s], phase)) ring.dead[parity] = 1;  // seen by all behind the barrier
@@ -434,7 +433,11 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_bwd_ring_kernel(const NormBwd
         }
     }
     th.write_dw(p, blockIdx.x, gridDim.x);
-    if (threadIdx.x == 0) drain_loads(ring.full, nullptr, p.stages, issued);  // no copy lands after this CTA exits
+    if (row < p.R && threadIdx.x == 0) {
+        // a wait ran out: no copy of the rows ahead lands after this CTA exits
+        const int64_t done = (row - blockIdx.x) / gridDim.x, rows = (p.R - 1 - blockIdx.x) / gridDim.x + 1;
+        drain_loads(ring.full, nullptr, p.stages, (int)min(done + p.stages, rows));
+    }
 }
 
 // dw[c] (+)= the sum of column c of the n partial rows, in a fixed order: 32
