@@ -894,7 +894,14 @@ __device__ __forceinline__ void load_group_tiles(const GroupMaps& maps, const Qu
     if (lane == 0) drain_loads(ring.full, nullptr, STAGES, i);  // no load lands after this CTA exits
 }
 
-// Rows of stage s's segment h (compute warps).
+// Rows of stage s's segment h (compute warps). What all lanes of a warp do
+// together (their transposing loads are the whole warp's) goes by group_cut,
+// which is the same for them all: whether a segment of the tile ends early.
+template <int STAGES, int STAGE_BYTES, int SEGS, int SEG_ROWS>
+__device__ __forceinline__ bool group_cut(const uint8_t* tiles, int s) {
+    const int* rows = reinterpret_cast<const GroupSmem<STAGES>*>(tiles + STAGES * STAGE_BYTES)->rows[s];
+    return (SEGS == 1 ? rows[0] : min(rows[0], rows[1])) < SEG_ROWS;
+}
 template <int STAGES, int STAGE_BYTES>
 __device__ __forceinline__ int group_seg_rows(const uint8_t* tiles, int s, int h) {
     return reinterpret_cast<const GroupSmem<STAGES>*>(tiles + STAGES * STAGE_BYTES)->rows[s][h];
@@ -1323,7 +1330,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t stage_base = smem_u32(tiles) + (uint32_t)(s * STAGE_BYTES);
         int valid = G;  // rows in groups: of this thread's G rows, those that are the group's
         if constexpr (GROUPED) valid = group_seg_rows<STAGES, STAGE_BYTES>(tiles, s, 0) - G * q;
-        const bool cut = GROUPED && __any_sync(0xffffffffu, valid < G);  // (the loads below are the whole warp's)
+        bool cut = false;
+        if constexpr (GROUPED) cut = group_cut<STAGES, STAGE_BYTES, 1, TILE_ROWS>(tiles, s);
         if constexpr (kSharedQuads) {
             if (shared_quads && quad_half == 0) {
                 int qtr = w.tr, qtc = w.tc;
@@ -1713,7 +1721,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<STAGES>)
         const uint32_t stage_base = smem_u32(tiles) + (uint32_t)(s * STAGE_BYTES) + lm_base;
         int valid = 64;  // rows in groups: of this thread's band, those that are the group's
         if constexpr (GROUPED) valid = group_seg_rows<STAGES, STAGE_BYTES>(tiles, s, q >> 1) - 64 * (q & 1);
-        const bool cut = GROUPED && __any_sync(0xffffffffu, valid < 64);  // (the loads below are the whole warp's)
+        bool cut = false;
+        if constexpr (GROUPED) cut = group_cut<STAGES, STAGE_BYTES, 2, 128>(tiles, s);
         uint32_t codes[8];
         uint32_t scodes[64 / NB];
         uint32_t scw = 0;
@@ -1876,7 +1885,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             valid = group_seg_rows<STAGES, STAGE_BYTES>(tiles, s, (lane & 3) >> 1) - 64 * (lane & 1);
             none = BandOrder::row(tid & 127) >= group_seg_rows<STAGES, STAGE_BYTES>(tiles, s, warp >> 2);
         }
-        const bool cut = GROUPED && __any_sync(0xffffffffu, valid < 64);  // (the loads below are the whole warp's)
+        bool cut = false;
+        if constexpr (GROUPED) cut = group_cut<STAGES, STAGE_BYTES, 2, 128>(tiles, s);
         auto load_col = [&](int n) {
             uint4 v;
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
