@@ -94,13 +94,11 @@ __device__ __forceinline__ void group_epilogue(const GroupedParams& p, const CUt
                                                Release release) {
     // 32 words (128 bytes) of each lane's row, from column x: a whole box of 32
     // rows through shared memory (128-byte swizzle) by TMA, which clips the
-    // columns past N. The warp leaves it together: the next loads from tensor
-    // memory are the whole warp's.
+    // columns past N
     const uint32_t rbase = obox + (uint32_t)lane * 128u;
     auto box = [&](const uint32_t* v, int x) {
         if (nv < 32) {
             if (lane < nv) store_row_words(p, v, row + lane, x);
-            __syncwarp();
             return;
         }
         if (lane == 0) bulk_wait_group_read0();  // the box's last store has read it
@@ -117,8 +115,8 @@ __device__ __forceinline__ void group_epilogue(const GroupedParams& p, const CUt
                 tma_store_2d(tmD, obox, x, row);
             bulk_commit_group();
         }
-        __syncwarp();
     };
+    __syncwarp();  // loads from tensor memory are the whole warp's
     if (!p.out_f32) {
         uint32_t w[64];
 #pragma unroll
@@ -150,6 +148,7 @@ __device__ __forceinline__ void group_epilogue(const GroupedParams& p, const CUt
         tc_wait_ld();
         scaled(acc);
         box(acc, n0);
+        __syncwarp();
         tmem_ld_32x32b_x32(taddr + 32, acc);
         tmem_ld_32x32b_x32(taddr + 64, acc + 32);
         tmem_ld_32x32b_x32(taddr + 96, acc + 64);
@@ -520,6 +519,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t acc[64];
+                __syncwarp();  // loads from tensor memory are the whole warp's
                 tmem_ld_32x32b_x32(taddr + 64 * h, acc);
                 tmem_ld_32x32b_x32(taddr + 64 * h + 32, acc + 32);
                 tc_wait_ld();
@@ -540,7 +540,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         store_row_words(p, acc + 32, row, n0 + 64 * h + 32);
                     }
                 }
-                __syncwarp();  // the next loads from tensor memory are the whole warp's
             }
         }
     }
