@@ -342,7 +342,9 @@ struct NormBwdThread {
 };
 
 // C <= 512: a row belongs to one warp, loads straight to registers, the next
-// row's before this row's sum is joined.
+// row's before this row's sum is joined. There are as many warps as rows of
+// weight gradients (kMaxNormPartials, four per SM), so that one CTA runs on an SM
+// and few rows are on their way: 65536 x 256 with dh, floor 21 us, takes 81.
 template <int NV>
 __global__ void __launch_bounds__(128, 4) rmsnorm_bwd_warp_kernel(const NormBwdParams p) {
     const int lane = threadIdx.x & 31;
@@ -382,6 +384,8 @@ __global__ void __launch_bounds__(128, 4) rmsnorm_bwd_warp_kernel(const NormBwdP
 // one row each), so that several rows per SM are in flight without registers
 // to hold them (16384 x 4096 with dh, 537 MB: 78 us and 4.5 for the weight
 // gradient's join; 187 with the rows loaded to registers when they are due).
+// Past 8192 columns a CTA has more than 512 threads, at most 64 registers each,
+// and spills: 4096 x 16384 with dh, floor 82 us, takes 163.
 template <int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) rmsnorm_bwd_ring_kernel(const NormBwdParams p) {
     extern __shared__ __align__(1024) uint8_t dyn_smem[];
@@ -474,12 +478,17 @@ cudaError_t launch_norm_ring(Kern kern, int grid, int threads, int smem, const P
     return launch_pdl(kern, dim3(grid), dim3(threads), (size_t)smem, s, p);
 }
 
-// 768 threads per SM with 16 elements each (68-80 registers), 512 with 32
-// (about 124), and no more CTAs than amax partials. Measured with the amax on
-// 16384 x 4096, 537 MB: 84 us with 16 elements and 32-byte accesses; 91 with 32
-// elements, 90 with 32 and 16-byte accesses; 99 with the rows in a ring as in
-// the backward pass (here half the traffic is stores, and more loads in flight
-// delay them). Into MXFP4, 4099 x 5120, 179 MB: 31 us, 35 with 16-byte accesses.
+// Where a row is a CTA's, 768 threads per SM with 16 elements each (63 to 70
+// registers) and 512 with 32 (115 to 128), and no more CTAs than amax partials.
+// Measured with the amax on 16384 x 4096, 537 MB: 84 us with 16 elements and
+// 32-byte accesses; 91 with 32 elements, 90 with 32 and 16-byte accesses; 99
+// with the rows in a ring as in the backward pass (here half the traffic is
+// stores, and more loads in flight delay them). Into MXFP4, 4099 x 5120, 179 MB:
+// 31 us, 35 with 16-byte accesses.
+// Where a row is a warp's the same counts are launched, but a thread takes 100
+// registers with the 16-point amax and 138 to 147 with 32 elements: four of the
+// six CTAs per SM run at once, or three of the four, and the rest after them.
+// 65536 x 256, floors 21 and 22 us: 47 with the amax, 93 into MXFP4.
 template <int NH, bool QUANT, int NCH>
 cudaError_t launch_norm_fwd_t(NormParams p, float* amax, int sms, int* n_partials, cudaStream_t s) {
     constexpr int G = kNormChunk<NH, QUANT>;
